@@ -823,3 +823,9 @@ def gdn_bwd_dhu_varlen(q, k, w, do, dv, cu_seqlens, g=None, dht=None, scale=1.0,
                                 _stream(dev))
     _lib.check(rc, "gdn_bwd_dhu_varlen")
     return {"dv2": dv2, "dh": dh, "dh0": dh0}
+
+
+from . import layer  # noqa: E402  (it takes this module's helpers)
+from .layer import *  # noqa: E402,F401,F403
+
+__all__ += layer.__all__

@@ -21,6 +21,7 @@ P = ctypes.c_void_p
 I = ctypes.c_int
 U = ctypes.c_uint
 F = ctypes.c_float
+L = ctypes.c_int64
 SZ = ctypes.c_size_t
 
 # name -> (restype, argtypes), mirroring include/gdn.h
@@ -67,6 +68,31 @@ SIGNATURES = {
     "gdn_bwd_dhu_varlen_workspace_bytes": (SZ, [I, I]),
     "gdn_bwd_dhu_varlen": (I, [P, P, P, P, P, P, P, P, F, P, P, I, P, P, P, I, I, I, I, I, P,
                                SZ, P]),
+    # layer operators
+    "causal_conv_fwd": (I, [P, L, P, P, P, P, P, I, I, I, I, I, I, P]),
+    "causal_conv_fwd_varlen": (I, [P, L, P, P, P, P, I, P, P, P, I, I, I, I, I, P]),
+    "causal_conv_bwd_workspace_bytes": (SZ, [I, I, I]),
+    "causal_conv_bwd": (I, [P, L, P, L, P, P, P, P, P, P, P, P, I, I, I, I, I, I, P, SZ, P]),
+    "causal_conv_bwd_varlen": (I, [P, L, P, L, P, P, P, P, I, P, P, P, P, P, P, I, I, I, I, I, P, SZ,
+                                   P]),
+    "causal_conv_step": (I, [P, L, P, P, P, P, P, I, I, I, I, I, I, P]),
+    "ssm_scan_fwd_workspace_bytes": (SZ, [I, I, I, I]),
+    "ssm_scan_fwd": (I, [P, L, P, L, P, P, L, P, L, P, P, L, P, P, P, P, P, I, I, I, I, I, I, P, SZ,
+                         P]),
+    "ssm_scan_fwd_varlen_workspace_bytes": (SZ, [P, I, I, I]),
+    "ssm_scan_fwd_varlen": (I, [P, L, P, L, P, P, L, P, L, P, P, I, P, P, L, P, P, P, P, P, I, I, I, I,
+                                I, P, SZ, P]),
+    "ssm_scan_bwd_workspace_bytes": (SZ, [I, I, I, I]),
+    "ssm_scan_bwd": (I, [P, L, P, P, L, P, L, P, P, L, P, L, P, P, L, P, P] + [P] * 9
+                     + [I, I, I, I, I, I, P, SZ, P]),
+    "ssm_scan_bwd_varlen_workspace_bytes": (SZ, [P, I, I, I]),
+    "ssm_scan_bwd_varlen": (I, [P, L, P, P, L, P, L, P, P, L, P, L, P, P, I, P, P, L, P, P] + [P] * 9
+                            + [I, I, I, I, I, P, SZ, P]),
+    "ssm_step": (I, [P, L, P, L, P, P, L, P, L, P, P, L, P, P, P, P, I, I, I, I, I, I, P]),
+    "rms_norm_fwd": (I, [P, L, P, L, P, F, P, P, P, I, I, I, I, P]),
+    "rms_norm_q8_fwd": (I, [P, L, P, L, P, F, I, P, P, P, I, I, I, I, P]),
+    "rms_norm_bwd_workspace_bytes": (SZ, [I, I]),
+    "rms_norm_bwd": (I, [P, L, P, L, P, P, P, L, P, P, P, I, I, I, I, P, SZ, P]),
 }
 
 _lib = None

@@ -15,10 +15,15 @@
 #include "../../include/gdn.h"
 #include "gdn_bwd_params.h"
 #include "gdn_internal.h"
+#include "gdn_layer.h"
 
 namespace {
 
 thread_local char g_err[512];
+
+}  // namespace
+
+namespace gdn {
 
 int fail(int code, const char* fmt, ...) {
   va_list ap;
@@ -36,6 +41,23 @@ int ok() {
 int hip_fail(hipError_t e, const char* what) {
   return fail(GDN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+int check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (need == 0) return GDN_OK;
+  if (!ws || bytes < need)
+    return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu", need, ws ? bytes : (size_t)0);
+  if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(GDN_ERR_INVALID, "workspace must be 256-byte aligned");
+  return GDN_OK;
+}
+
+}  // namespace gdn
+
+namespace {
+
+using gdn::check_workspace;
+using gdn::fail;
+using gdn::hip_fail;
+using gdn::ok;
 
 bool kv_supported(int dtype, int K, int V, bool per_key) {
   if (V != 64 && V != 128) return false;
@@ -77,14 +99,6 @@ unsigned fwd_flags(const float* gk, const void* h_chunks, const void* v_new) {
 // keeps every per-chunk term on chip (its only scratch is the rank table of a packed batch).
 bool fused_path(int dtype, unsigned flags) {
   return dtype == GDN_DTYPE_BF16 && !(flags & (GDN_FWD_PER_KEY | GDN_FWD_SAVES));
-}
-
-int check_workspace(const void* ws, size_t bytes, size_t need) {
-  if (need == 0) return GDN_OK;
-  if (!ws || bytes < need)
-    return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu", need, ws ? bytes : (size_t)0);
-  if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(GDN_ERR_INVALID, "workspace must be 256-byte aligned");
-  return GDN_OK;
 }
 
 }  // namespace

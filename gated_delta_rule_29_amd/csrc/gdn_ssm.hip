@@ -1,0 +1,217 @@
+// gdn_ssm.hip -- the selective state space scan: for prompts (dense or packed sequences, initial and
+// final states, states saved for the backward pass) and for single tokens on a cache of states.
+//
+//   de_t = softplus(dt_t + dt_bias)   (or dt_t + dt_bias)
+//   h_t[d,n] = e^{de_t[d] A[d,n]} h_{t-1}[d,n] + de_t[d] x_t[d] B_t[n]
+//   y_t[d] = (sum_n C_t[n] h_t[d,n] + skip[d] x_t[d]) * (z_t[d] sigmoid(z_t[d]) if z)
+//
+// Layout.  LN lanes hold a channel's N states, NPL each (N padded to LN * NPL with zeros), so a wave
+// holds 64 / LN channels.  Lane j of a channel also owns every LN-th token: it loads that token's x,
+// dt and z and forms its step size, gate and output once, and the channel's other lanes read the
+// two values they need through lane-exchange operands.  B and C, shared by all channels, are staged as
+// fp32 in LDS, 32 tokens at a time.  Everything is fp32 but the inputs' and outputs' own types.
+//
+// Long sequences are cut into segments where there are too few channels to fill the chip: a first
+// kernel forms each segment's end state from a zero start, a second joins them (a segment's whole
+// decay is e^{A sum(de)}), and the scan proper then runs all segments at once.
+#include "../../include/gdn.h"
+#include "gdn_ssm_device.h"
+
+namespace gdn {
+
+namespace {
+
+// SUMMARY: only the state from a zero start and the summed step sizes of a segment.
+template <typename T, int LN, int NPL, bool SUMMARY>
+__global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
+  constexpr int NP = LN * NPL, CH = 64 / LN, TL = kSsmChunk / LN;
+  __shared__ __align__(16) float bc[kSsmChunk * NP * 2];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int j = lane % LN, seg = blockIdx.x / groups;
+  const int c = ((blockIdx.x - seg * groups) * 4 + wv) * CH + lane / LN;
+  const bool cv = c < p.D;
+  const int cc = cv ? c : p.D - 1;  // loads of the lanes past the last channel stay inside
+  const Piece pc = find_piece(p.s, seg, p.seg, lane);
+  if (pc.seq < 0) return;
+  const int t0 = pc.begin + pc.k * p.seg, t1 = min(t0 + p.seg, pc.end);
+  if (SUMMARY && t1 == pc.end) return;  // nothing follows the last segment
+
+  float A2[NPL], h[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int n = j * NPL + i;
+    A2[i] = n < p.N ? p.A[(int64_t)cc * p.N + n] * kLog2e : 0.f;
+  }
+  load_state<NPL>(SUMMARY ? nullptr : p.seg_state ? p.seg_state + (int64_t)seg * p.D * p.N
+                  : p.h0 ? p.h0 + (int64_t)pc.seq * p.D * p.N : nullptr, cc, j, p.N, h);
+  const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f, skip = p.skip ? p.skip[cc] : 0.f;
+  float dsum = 0.f;
+  int64_t chunk = 0;
+  if (!SUMMARY && p.h) chunk = find_piece_before(p.s, pc, kSsmChunk, lane) + (t0 - pc.begin) / kSsmChunk;
+
+  for (int tb = t0; tb < t1; tb += kSsmChunk) {
+    __syncthreads();
+    stage_bc<T, NP>(p, tb, t1, bc);
+    if (!SUMMARY && p.h) {
+      if (cv) store_state<NPL>(p.h + chunk * p.D * p.N, c, j, p.N, h);
+      ++chunk;
+    }
+    float xr[TL], dr[TL], zr[TL];
+#pragma unroll
+    for (int g = 0; g < TL; ++g) {
+      const int t = tb + g * LN + j;
+      const bool v = t < t1;
+      xr[g] = v ? to_f(static_cast<const T*>(p.x)[t * p.x_pitch + cc]) : 0.f;
+      dr[g] = v ? to_f(static_cast<const T*>(p.dt)[t * p.dt_pitch + cc]) : 0.f;
+      zr[g] = !SUMMARY && p.z && v ? to_f(static_cast<const T*>(p.z)[t * p.z_pitch + cc]) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < TL; ++g) {
+      const int t = tb + g * LN + j;
+      float de = dr[g] + bias;
+      if (p.softplus) de = softplus_f(de, nullptr);
+      if (t >= t1) de = 0.f;  // a token behind the end keeps the state as it is
+      const float dx = de * xr[g];
+      dsum += de;
+      float yp[LN];
+      static_for<LN>([&](auto k) {
+        const float dk = lane_of<LN, k()>(de), xk = lane_of<LN, k()>(dx);
+        float b[NPL], cf[NPL];
+        read_bc<NPL>(bc + ((g * LN + k()) * NP + j * NPL) * 2, b, cf);
+        float acc = 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+          h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dk * A2[i]), h[i], xk * b[i]);
+          if (!SUMMARY) acc = __builtin_fmaf(cf[i], h[i], acc);
+        }
+        yp[k()] = acc;
+      });
+      if (!SUMMARY) {
+        float y = reduce_scatter<LN>(yp, j) + skip * xr[g];
+        if (p.z) y *= zr[g] * sigmoid_f(zr[g]);
+        if (cv && t < t1) static_cast<T*>(p.y)[(int64_t)t * p.D + c] = to_t<T>(y);
+      }
+    }
+  }
+  if (SUMMARY) {
+    if (cv) store_state<NPL>(p.seg_state + (int64_t)seg * p.D * p.N, c, j, p.N, h);
+    dsum = group_sum<LN>(dsum);
+    if (cv && j == 0) p.seg_sum[(int64_t)seg * p.D + c] = dsum;
+  } else if (p.ht && t1 == pc.end && cv) {
+    store_state<NPL>(p.ht + (int64_t)pc.seq * p.D * p.N, c, j, p.N, h);
+  }
+}
+
+// A sequence's segments in order: seg_state becomes the state at each segment's start.
+__global__ __launch_bounds__(256) void ssm_join_kernel(SsmParams p, int per_seq) {
+  const int seq = blockIdx.x / per_seq;
+  const int64_t e = (int64_t)(blockIdx.x - seq * per_seq) * 256 + threadIdx.x;
+  const int lane = threadIdx.x & 63;
+  const int64_t DN = (int64_t)p.D * p.N;
+  const SeqPieces sp = pieces_of(p.s, seq, p.seg, lane);
+  if (e >= DN) return;
+  const int64_t d = e / p.N;
+  const float a = p.A[e] * kLog2e;
+  float h = p.h0 ? p.h0[seq * DN + e] : 0.f;
+  for (int i = 0; i < sp.count; ++i) {
+    const int64_t s = sp.first + i;
+    const bool last = i == sp.count - 1;
+    const float own = last ? 0.f : p.seg_state[s * DN + e], sum = last ? 0.f : p.seg_sum[s * p.D + d];
+    p.seg_state[s * DN + e] = h;
+    h = __builtin_fmaf(__builtin_amdgcn_exp2f(a * sum), h, own);
+  }
+}
+
+// One token a row.  A row whose slot is outside the cache, or is an earlier row's, changes nothing
+// and gives 0.
+template <typename T, int LN, int NPL>
+__global__ __launch_bounds__(256) void ssm_step_kernel(SsmStepParams p, int groups) {
+  constexpr int CH = 64 / LN;
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, j = lane % LN;
+  const int b = blockIdx.x / groups;
+  const int c = ((blockIdx.x - b * groups) * 4 + wv) * CH + lane / LN;
+  const bool cv = c < p.D;
+  const int slot = p.slots ? p.slots[b] : b;
+  bool live = slot >= 0 && slot < p.S;
+  float h[NPL];
+  float* st = p.state + (live ? (int64_t)slot * p.D * p.N : 0);
+  if (live && cv) load_state<NPL>(st, c, j, p.N, h);
+  if (p.slots && live) live = !slot_taken(p.slots, b, slot);  // slot is the workgroup's
+  if (!cv) return;
+  float y = 0.f;
+  if (live) {
+    const float x = to_f(static_cast<const T*>(p.x)[b * p.x_pitch + c]);
+    float de = to_f(static_cast<const T*>(p.dt)[b * p.dt_pitch + c]) + (p.dt_bias ? p.dt_bias[c] : 0.f);
+    if (p.softplus) de = softplus_f(de, nullptr);
+    const float dx = de * x;
+    float acc = 0.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const int n = j * NPL + i;
+      if (n < p.N) {
+        const float bn = to_f(static_cast<const T*>(p.Bm)[b * p.b_pitch + n]);
+        const float cn = to_f(static_cast<const T*>(p.Cm)[b * p.c_pitch + n]);
+        const float a = __builtin_amdgcn_exp2f(de * (p.A[(int64_t)c * p.N + n] * kLog2e));
+        h[i] = __builtin_fmaf(a, h[i], dx * bn);
+        acc = __builtin_fmaf(cn, h[i], acc);
+      }
+    }
+    store_state<NPL>(st, c, j, p.N, h);
+    y = group_sum<LN>(acc) + (p.skip ? p.skip[c] * x : 0.f);
+    if (p.z) {
+      const float z = to_f(static_cast<const T*>(p.z)[b * p.z_pitch + c]);
+      y *= z * sigmoid_f(z);
+    }
+  }
+  if (j == 0) static_cast<T*>(p.y)[(int64_t)b * p.D + c] = to_t<T>(y);
+}
+
+}  // namespace
+
+int ssm_segment(bool backward, int rows, int nseq, int max_len, int D, int N) {
+  const int ch = N <= 16 ? 16 : 4;  // channels of a wave
+  const int64_t per_seg = (D + ch - 1) / ch;
+  const int round = (max_len + kSsmChunk - 1) / kSsmChunk * kSsmChunk;
+  if (per_seg * nseq >= 1024 || max_len <= 4 * kSsmChunk) return round;
+  const int64_t want = (2048 + per_seg - 1) / per_seg;  // segments in all
+  int64_t seg = (rows + want - 1) / want;
+  seg = (seg + kSsmChunk - 1) / kSsmChunk * kSsmChunk;
+  if (seg < 4 * kSsmChunk) seg = 4 * kSsmChunk;
+  return seg >= round ? round : (int)seg;
+}
+
+size_t ssm_fwd_ws_bytes(int nseg, int D, int N) { return (size_t)nseg * D * (N + 1) * 4; }
+
+hipError_t launch_ssm_fwd(SsmParams p, int dtype, void* ws, hipStream_t st) {
+  const bool split = p.nseg > p.s.n;
+  p.seg_state = split ? static_cast<float*>(ws) : nullptr;
+  p.seg_sum = split ? p.seg_state + (int64_t)p.nseg * p.D * p.N : nullptr;
+  return ssm_dispatch(dtype, p.N, [&](auto t, auto ln, auto npl) {
+    using T = decltype(t);
+    constexpr int LN = decltype(ln)::value, NPL = decltype(npl)::value;
+    const int groups = (p.D + 4 * (64 / LN) - 1) / (4 * (64 / LN));
+    const dim3 grid((unsigned)(groups * p.nseg));
+    hipError_t e;
+    if (split) {
+      ssm_fwd_kernel<T, LN, NPL, true><<<grid, 256, 0, st>>>(p, groups);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      const int per_seq = (int)(((int64_t)p.D * p.N + 255) / 256);
+      ssm_join_kernel<<<dim3((unsigned)(per_seq * p.s.n)), 256, 0, st>>>(p, per_seq);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    ssm_fwd_kernel<T, LN, NPL, false><<<grid, 256, 0, st>>>(p, groups);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_ssm_step(const SsmStepParams& p, int dtype, hipStream_t st) {
+  return ssm_dispatch(dtype, p.N, [&](auto t, auto ln, auto npl) {
+    constexpr int LN = decltype(ln)::value, NPL = decltype(npl)::value;
+    const int groups = (p.D + 4 * (64 / LN) - 1) / (4 * (64 / LN));
+    ssm_step_kernel<decltype(t), LN, NPL><<<dim3((unsigned)(groups * p.B)), 256, 0, st>>>(p, groups);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace gdn

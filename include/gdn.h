@@ -25,14 +25,20 @@
  *    backward of its scan (cam_scan_bwd) and of its prep (cam_prep_bwd); the backward of a BiGDN direction (bigdn_dir_bwd),
  *    of the block's merge (bigdn_merge_bwd) and of its front end (gdn_prep_bwd);
  *  - the backward's inputs (gdn_bwd_prep) and state-gradient pass (gdn_bwd_dhu,
- *    gdn_bwd_dhu_varlen).
+ *    gdn_bwd_dhu_varlen);
+ *  - the layer operators around a recurrent scan, each with its gradient and its single-token
+ *    form where it has one: the short causal convolution (causal_conv_*), the selective state
+ *    space scan (ssm_scan_*, ssm_step) and the residual RMS norm with an 8-bit output
+ *    (rms_norm_*).
  *
  * Conventions shared by every entry point.
  *  - All tensor pointers are DEVICE pointers unless the name ends in _host.  The caller owns
  *    all memory, including any workspace; the library keeps no device allocation between
  *    calls and has no other global mutable state, except the static scratch array of
  *    gdn_fwd_varlen_noalloc (one per GPU, held until the process ends).
- *  - Tensors are dense and row-major in the shapes given (no strides).
+ *  - Tensors are dense and row-major in the shapes given (no strides).  The layer operators
+ *    take a pitch for their row inputs: the elements from one token's row to the next (at
+ *    least the row's width), so that columns of a wider tensor are read in place.
  *  - dtype: GDN_DTYPE_F32 (fp32 inputs, fp32 MFMA, fp32 state) or GDN_DTYPE_BF16 (bf16 q/k/v
  *    and bf16 outputs, bf16 MFMA operands, fp32 accumulation and fp32 state).  Gates (g, gk,
  *    beta), initial and final states are always fp32.  Gates are natural-log decays: a base-2
@@ -49,6 +55,7 @@
 #define GDN_H_
 
 #include <stddef.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -619,6 +626,191 @@ GDN_API int gdn_bwd_dhu_varlen(const void* q, const void* k, const void* w, cons
                                float* dh_chunks, void* dv2, float* dh0, int T_total, int H,
                                int K, int V, int dtype, void* workspace, size_t workspace_bytes,
                                void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Layer operators.  Conventions beside the shared ones:
+ *  - x [tokens, C] with a pitch: row r starts at x + r * pitch elements.  A dense batch of B
+ *    sequences of T tokens has rows b * T + t; a packed batch (_varlen) has T_total rows,
+ *    sequence i covering rows [cu[i], cu[i+1]), with cu_seqlens and cu_seqlens_host as in
+ *    gdn_fwd_varlen.  Outputs are dense.
+ *  - dtype is that of the activations (inputs and outputs that are not said to be fp32);
+ *    all arithmetic, states and sums over tokens or channels are fp32, each result rounded once.
+ *  - Pointers have their type's alignment; 16-byte alignment (and pitches and widths that are
+ *    multiples of 16 bytes) is faster.  fp32 state tensors [.., D, N] must be 16-byte
+ *    aligned where N is a multiple of 4.
+ *  - Sums over rows and channels are joined in a fixed order: results are deterministic.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * causal_conv_fwd -- short causal convolution, one filter a channel:
+ *     u_t[d] = bias[d] + sum_{i<W} w[d,i] x_{t-(W-1)+i}[d],   y = silu ? u sigmoid(u) : u
+ * where rows before a sequence's first token are init's (oldest first).
+ *   x      [B, T, D] (x_pitch)      w [D, W] fp32      bias [D] fp32 or NULL (0)
+ *   init   [B, W-1, D] or NULL (0): the W-1 tokens before the first one
+ *   y      [B, T, D] OUT
+ *   last   [B, W-1, D] OUT or NULL: the last W-1 tokens (init's among them where T < W-1),
+ *          the init of the call that continues the sequences
+ * Supported: W in {2, 3, 4} (GDN_ERR_UNSUPPORTED otherwise).
+ */
+GDN_API int causal_conv_fwd(const void* x, int64_t x_pitch, const float* w, const float* bias,
+                            const void* init, void* y, void* last, int B, int T, int D, int W,
+                            int silu, int dtype, void* stream);
+/* The packed form: x, y [1, T_total, D], init and last [N, W-1, D]. */
+GDN_API int causal_conv_fwd_varlen(const void* x, int64_t x_pitch, const float* w,
+                                   const float* bias, const int* cu_seqlens,
+                                   const int* cu_seqlens_host, int N, const void* init, void* y,
+                                   void* last, int T_total, int D, int W, int silu, int dtype,
+                                   void* stream);
+
+/*
+ * causal_conv_bwd -- gradient of causal_conv_fwd from its inputs, dy and (or NULL: 0) dlast.
+ *   dx [B, T, D] OUT;  dinit [B, W-1, D] OUT or NULL;  dw [D, W] fp32 OUT;
+ *   dbias [D] fp32 OUT or NULL
+ *   workspace  at least causal_conv_bwd_workspace_bytes(tokens in all, D, W), 256-byte aligned
+ */
+GDN_API size_t causal_conv_bwd_workspace_bytes(int T_total, int D, int W);
+GDN_API int causal_conv_bwd(const void* dy, int64_t dy_pitch, const void* x, int64_t x_pitch,
+                            const float* w, const float* bias, const void* init,
+                            const void* dlast, void* dx, void* dinit, float* dw, float* dbias,
+                            int B, int T, int D, int W, int silu, int dtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
+GDN_API int causal_conv_bwd_varlen(const void* dy, int64_t dy_pitch, const void* x,
+                                   int64_t x_pitch, const float* w, const float* bias,
+                                   const int* cu_seqlens, const int* cu_seqlens_host, int N,
+                                   const void* init, const void* dlast, void* dx, void* dinit,
+                                   float* dw, float* dbias, int T_total, int D, int W, int silu,
+                                   int dtype, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * causal_conv_step -- causal_conv_fwd for one token a row, on a cache of S slots.
+ *   x [B, D] (x_pitch);  state [S, W-1, D] IN/OUT: a slot's last W-1 tokens, moved on by one
+ *   slots [B] int32 (device): the slot of each row; NULL: row b uses slot b (then S >= B).
+ *   A row whose slot is outside [0, S) (a padded row) changes nothing and its y is 0.  So does
+ *   a row that names the slot of an earlier row: the first row of a slot is the one that counts.
+ *   y [B, D] OUT
+ */
+GDN_API int causal_conv_step(const void* x, int64_t x_pitch, const float* w, const float* bias,
+                             void* state, const int* slots, void* y, int B, int S, int D, int W,
+                             int silu, int dtype, void* stream);
+
+/*
+ * ssm_scan_fwd -- selective state space scan, a state of N values a channel:
+ *     de_t = softplus ? log(1 + e^{dt_t + dt_bias}) : dt_t + dt_bias
+ *     h_t[d,n] = e^{de_t[d] A[d,n]} h_{t-1}[d,n] + de_t[d] x_t[d] Bm_t[n]
+ *     y_t[d] = (sum_n Cm_t[n] h_t[d,n] + skip[d] x_t[d]) * (z ? z_t[d] sigmoid(z_t[d]) : 1)
+ *   x, dt, z  [B, T, D] (a pitch each; z NULL: no gate)
+ *   A         [D, N] fp32 (natural; negative for a decay)
+ *   Bm, Cm    [B, T, N] (a pitch each), shared by all channels
+ *   skip, dt_bias [D] fp32 or NULL (0);  h0 [B, D, N] fp32 or NULL (0)
+ *   y  [B, T, D] OUT;  ht [B, D, N] fp32 OUT or NULL: the state after the last token
+ *   h  [B, NC, D, N] fp32 OUT or NULL: the state entering each chunk of GDN_SSM_CHUNK tokens,
+ *      NC = ceil(T / GDN_SSM_CHUNK) (what ssm_scan_bwd needs)
+ *   workspace  at least ssm_scan_fwd_workspace_bytes (0 where the sequences are not cut),
+ *      256-byte aligned
+ * Where the channels alone do not fill the chip, long sequences are cut into segments that are
+ * joined by their states; results then differ from the uncut order in fp32 rounding only.
+ * Supported: 1 <= N <= 64 (GDN_ERR_UNSUPPORTED otherwise), any D and T >= 1.
+ */
+#define GDN_SSM_CHUNK 32
+GDN_API size_t ssm_scan_fwd_workspace_bytes(int B, int T, int D, int N);
+GDN_API int ssm_scan_fwd(const void* x, int64_t x_pitch, const void* dt, int64_t dt_pitch,
+                         const float* A, const void* Bm, int64_t b_pitch, const void* Cm,
+                         int64_t c_pitch, const float* skip, const void* z, int64_t z_pitch,
+                         const float* dt_bias, const float* h0, void* y, float* ht, float* h,
+                         int B, int T, int D, int N, int softplus, int dtype, void* workspace,
+                         size_t workspace_bytes, void* stream);
+/* The packed form: tokens [1, T_total, .], h0 and ht [N_seq, D, N]; h [1, NC_total, D, N] with the
+ * sequences' chunks in order, NC_total = sum_i ceil(length_i / GDN_SSM_CHUNK). */
+GDN_API size_t ssm_scan_fwd_varlen_workspace_bytes(const int* cu_seqlens_host, int N_seq, int D,
+                                                   int N);
+GDN_API int ssm_scan_fwd_varlen(const void* x, int64_t x_pitch, const void* dt, int64_t dt_pitch,
+                                const float* A, const void* Bm, int64_t b_pitch, const void* Cm,
+                                int64_t c_pitch, const int* cu_seqlens,
+                                const int* cu_seqlens_host, int N_seq, const float* skip,
+                                const void* z, int64_t z_pitch, const float* dt_bias,
+                                const float* h0, void* y, float* ht, float* h, int T_total,
+                                int D, int N, int softplus, int dtype, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
+ * ssm_scan_bwd -- gradient of ssm_scan_fwd from its inputs, the states h that it saved, dy and (or
+ * NULL: 0) dht.  (h0 is h's first state and not needed.)
+ *   dx, ddt [B, T, D] OUT, dz [B, T, D] OUT (NULL if and only if z is);  dA [D, N] fp32 OUT
+ *   dBm, dCm [B, T, N] OUT;  dskip, ddt_bias [D] fp32 OUT or NULL;  dh0 [B, D, N] fp32 OUT or NULL
+ *   workspace  at least ssm_scan_bwd_workspace_bytes, 256-byte aligned
+ */
+GDN_API size_t ssm_scan_bwd_workspace_bytes(int B, int T, int D, int N);
+GDN_API int ssm_scan_bwd(const void* dy, int64_t dy_pitch, const float* h, const void* x,
+                         int64_t x_pitch, const void* dt, int64_t dt_pitch, const float* A,
+                         const void* Bm, int64_t b_pitch, const void* Cm, int64_t c_pitch,
+                         const float* skip, const void* z, int64_t z_pitch, const float* dt_bias,
+                         const float* dht, void* dx, void* ddt, float* dA, void* dBm, void* dCm,
+                         float* dskip, void* dz, float* ddt_bias, float* dh0, int B, int T, int D,
+                         int N, int softplus, int dtype, void* workspace, size_t workspace_bytes,
+                         void* stream);
+GDN_API size_t ssm_scan_bwd_varlen_workspace_bytes(const int* cu_seqlens_host, int N_seq, int D,
+                                                   int N);
+GDN_API int ssm_scan_bwd_varlen(const void* dy, int64_t dy_pitch, const float* h, const void* x,
+                                int64_t x_pitch, const void* dt, int64_t dt_pitch,
+                                const float* A, const void* Bm, int64_t b_pitch, const void* Cm,
+                                int64_t c_pitch, const int* cu_seqlens,
+                                const int* cu_seqlens_host, int N_seq, const float* skip,
+                                const void* z, int64_t z_pitch, const float* dt_bias,
+                                const float* dht, void* dx, void* ddt, float* dA, void* dBm,
+                                void* dCm, float* dskip, void* dz, float* ddt_bias, float* dh0,
+                                int T_total, int D, int N, int softplus, int dtype,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ssm_step -- ssm_scan_fwd for one token a row, on a cache of S states.
+ *   x, dt, z [B, D], Bm, Cm [B, N] (a pitch each);  state [S, D, N] fp32 IN/OUT;  y [B, D] OUT
+ *   slots [B] int32 or NULL, as in causal_conv_step
+ */
+GDN_API int ssm_step(const void* x, int64_t x_pitch, const void* dt, int64_t dt_pitch,
+                     const float* A, const void* Bm, int64_t b_pitch, const void* Cm,
+                     int64_t c_pitch, const float* skip, const void* z, int64_t z_pitch,
+                     const float* dt_bias, float* state, const int* slots, void* y, int B, int S,
+                     int D, int N, int softplus, int dtype, void* stream);
+
+/*
+ * rms_norm_fwd -- root-mean-square norm with the residual's addition, over M rows of D:
+ *     s = x + residual, stored in the residual's type (s = x without a residual)
+ *     rstd = 1 / sqrt(mean_c s_c^2 + eps) of the stored s,   y_c = s_c rstd w_c
+ *   x [M, D] dtype (x_pitch);  residual [M, D] rdtype (r_pitch) or NULL;  w [D] fp32
+ *   y [M, D] dtype OUT;  sum [M, D] rdtype OUT (s; with a residual only, NULL: not written);
+ *   rstd [M] fp32 OUT or NULL
+ * rdtype: dtype, or GDN_DTYPE_F32 with bf16 activations (a residual stream in fp32).
+ * Supported: D <= 32768; eps > 0.
+ */
+GDN_API int rms_norm_fwd(const void* x, int64_t x_pitch, const void* residual, int64_t r_pitch,
+                         const float* w, float eps, void* y, void* sum, float* rstd, int M, int D,
+                         int dtype, int rdtype, void* stream);
+
+/*
+ * rms_norm_q8_fwd -- rms_norm_fwd with y in 8 bits (OCP e4m3: no infinity, largest 448):
+ *     scale = max(max |y|, 1e-12) / 448 over a row (block 0) or over each 128 columns (block 128;
+ *     the last block may be shorter),  q = e4m3(y / scale) to nearest even
+ *   q [M, D] bytes OUT;  scale [M, block ? ceil(D / 128) : 1] fp32 OUT.  A NaN in a row makes its
+ *   scales and values NaN.
+ */
+GDN_API int rms_norm_q8_fwd(const void* x, int64_t x_pitch, const void* residual, int64_t r_pitch,
+                            const float* w, float eps, int block, void* q, float* scale,
+                            void* sum, int M, int D, int dtype, int rdtype, void* stream);
+
+/*
+ * rms_norm_bwd -- gradient of rms_norm_fwd from the stored s (x itself without a residual) and
+ * rstd:  ds = rstd (dy w - s rstd^2 mean_c(dy w s)) + dsum
+ *   dy [M, D] dtype;  s [M, D] sdtype;  dsum [M, D] sdtype or NULL (0): gradient of the stored s
+ *   ds [M, D] sdtype OUT: the residual's gradient, and x's where the types agree
+ *   dx [M, D] dtype OUT or NULL: the same in x's type;  dw [D] fp32 OUT
+ *   workspace  at least rms_norm_bwd_workspace_bytes(M, D), 256-byte aligned
+ */
+GDN_API size_t rms_norm_bwd_workspace_bytes(int M, int D);
+GDN_API int rms_norm_bwd(const void* dy, int64_t dy_pitch, const void* s, int64_t s_pitch,
+                         const float* w, const float* rstd, const void* dsum, int64_t dsum_pitch,
+                         void* ds, void* dx, float* dw, int M, int D, int dtype, int sdtype,
+                         void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

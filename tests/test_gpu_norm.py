@@ -1,0 +1,123 @@
+"""GPU parity of the residual RMS norm, its 8-bit output and its gradient against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer as L
+from tests.gpu_util import say
+from tests.layer_util import DEV, TYPES, arr, check, gen, pitched, rn
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-5
+
+# rows, columns, (extra columns, offset)
+CASES = [(1, 1, (0, 0)), (1, 4096, (0, 0)), (5, 64, (0, 0)), (9, 200, (3, 1)), (7, 512, (8, 8)), (3, 520, (0, 0)),
+         (67, 2570, (0, 0)), (4, 4100, (5, 2)), (3, 6144, (16, 8)), (2, 16384, (0, 0)), (2, 17001, (0, 0)),
+         (2, 32768, (0, 0)), (300, 136, (0, 0))]
+
+
+def _inputs(M, D, pitch, dtype, rtype, seed):
+    g = gen(seed)
+    t, rt = TYPES[dtype], TYPES[rtype]
+    c = dict(x=rn(g, M, D, dtype=t), residual=(3 * rn(g, M, D)).to(rt), w=1 + 0.2 * rn(g, D), dy=rn(g, M, D, dtype=t),
+             dsum=rn(g, M, D, dtype=rt))
+    d = {k: v.to(DEV) for k, v in c.items()}
+    if pitch[0]:
+        for k in ("x", "residual", "dy", "dsum"):
+            d[k] = pitched(c[k], *pitch)
+    return c, d
+
+
+def _sum(c):
+    """The stored sum: fp32 addition, rounded to the residual's type."""
+    return (c["x"].float() + c["residual"].float()).to(c["residual"].dtype)
+
+
+@pytest.mark.parametrize("dtype,rtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_forward_and_gradient(case, dtype, rtype):
+    import gated_delta_rule_29_amd as g
+
+    M, D, pitch = CASES[case]
+    say("norm M %d D %d pitch %s %s residual %s" % (M, D, pitch, dtype, rtype))
+    c, d = _inputs(M, D, pitch, dtype, rtype, case)
+    out = g.rms_norm_fwd(d["x"], d["w"], residual=d["residual"], eps=EPS, want_rstd=True)
+    s = _sum(c)
+    assert torch.equal(out["sum"].cpu(), s)
+    y, rstd = L.norm(arr(s), arr(c["w"]), EPS)
+    check("y", out["y"], y)
+    check("rstd", out["rstd"], rstd)
+    alone = g.rms_norm_fwd(d["x"], d["w"], eps=EPS)
+    assert set(alone) == {"y"}
+    check("y alone", alone["y"], L.norm(arr(c["x"]), arr(c["w"]), EPS)[0])
+
+    s_in = pitched(s, *pitch) if pitch[0] else out["sum"]
+    gr = g.rms_norm_bwd(d["dy"], s_in, d["w"], out["rstd"], dsum=d["dsum"])
+    ref = L.norm_bwd(arr(c["dy"]), arr(s), arr(c["w"]), EPS, arr(c["dsum"]))
+    check("dx", gr["dx"], ref["ds"])
+    check("dresidual", gr["dresidual"], ref["ds"])
+    assert gr["dx"].dtype == TYPES[dtype] and gr["dresidual"].dtype == TYPES[rtype]
+    check("dw", gr["dw"], ref["dw"])
+    if D > 1:  # one column without eps cancels to rounding
+        gr = g.rms_norm_bwd(d["dy"], s_in, d["w"], out["rstd"])
+        check("dx without dsum", gr["dx"], L.norm_bwd(arr(c["dy"]), arr(s), arr(c["w"]), EPS)["ds"])
+
+
+def _half_step_e4m3(v):
+    """Half the distance between e4m3 values around |v| (below 2^-6 they are 2^-9 apart)."""
+    e = np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -6)))
+    return np.exp2(e - 4)
+
+
+@pytest.mark.parametrize("block", [0, 128])
+@pytest.mark.parametrize("dtype,rtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_eight_bits(case, dtype, rtype, block):
+    import gated_delta_rule_29_amd as g
+
+    M, D, pitch = CASES[case]
+    say("norm q8 M %d D %d pitch %s %s residual %s block %d" % (M, D, pitch, dtype, rtype, block))
+    c, d = _inputs(M, D, pitch, dtype, rtype, 100 + case)
+    out = g.rms_norm_q8_fwd(d["x"], d["w"], residual=d["residual"], eps=EPS, block=block)
+    s = _sum(c)
+    assert torch.equal(out["sum"].cpu(), s)
+    y, _ = L.norm(arr(s), arr(c["w"]), EPS)
+    scale = L.norm_scales(y, block)
+    check("scale", out["scale"], scale)
+    v = y / np.repeat(scale, block or D, 1)[:, :D]  # exact quotients, at most 448
+    q = arr(out["q"].float())
+    assert np.abs(q).max() <= 448
+    # nearest value, up to the fp32 roundings of y and the scale (16 u of the quotient)
+    assert (np.abs(q - v) <= _half_step_e4m3(np.maximum(np.abs(q), np.abs(v))) + 16 * 2.0 ** -24 * np.abs(v)).all()
+
+
+def test_eight_bits_of_zero_and_not_finite_rows():
+    import gated_delta_rule_29_amd as g
+
+    for D in (256, 1030):  # 16-byte vectors and single columns
+        say("norm q8 special rows D %d" % D)
+        x = torch.ones(4, D)
+        x[0] = 0.0
+        x[1, 5] = float("nan")
+        x[2, :128] = 0.0
+        for block in (0, 128):
+            o = g.rms_norm_q8_fwd(x.to(DEV), torch.ones(D, device=DEV), block=block)
+            q, sc = o["q"].float().cpu(), o["scale"].cpu()
+            assert not q[0].any() and (sc[0] == torch.tensor(1e-12) / 448).all()
+            assert q[1].isnan().all() and sc[1].isnan().all()
+            assert (q[3] == 448).all() and torch.isfinite(q[2]).all()
+            assert not q[2, :128].any() and (q[2, 128:] == 448).all()
+
+
+def test_gradient_over_many_rows_is_deterministic():
+    import gated_delta_rule_29_amd as g
+
+    say("norm gradient of many rows")
+    c, d = _inputs(5000, 96, (0, 0), "f32", "f32", 8)
+    o = g.rms_norm_fwd(d["x"], d["w"], residual=d["residual"], want_rstd=True)
+    a = g.rms_norm_bwd(d["dy"], o["sum"], d["w"], o["rstd"])
+    b = g.rms_norm_bwd(d["dy"], o["sum"], d["w"], o["rstd"])
+    ref = L.norm_bwd(arr(c["dy"]), arr(_sum(c)), arr(c["w"]), EPS)
+    check("dw", a["dw"], ref["dw"])
+    check("dx", a["dx"], ref["ds"])
+    assert torch.equal(a["dw"], b["dw"])
