@@ -70,8 +70,9 @@ hipError_t launch_conv_fwd(const ConvParams& p, int dtype, hipStream_t st);
 hipError_t launch_conv_bwd(const ConvBwdParams& p, int dtype, hipStream_t st);
 hipError_t launch_conv_step(const ConvStepParams& p, int dtype, hipStream_t st);
 
-// Tokens between two saved states of the selective scan.
-constexpr int kSsmChunk = 32;
+// Tokens between two saved states of the selective scan, and of a step of its forward kernels.
+constexpr int kSsmChunk = 16;
+constexpr int kSsmBlock = 32;
 constexpr int kSsmMaxN = 64;
 
 struct SsmParams {
@@ -91,7 +92,7 @@ struct SsmParams {
   Seqs s;
   int D, N;
   bool softplus;
-  // the split of long sequences: segments of `seg` tokens (a multiple of kSsmChunk), nseg in all
+  // the split of long sequences: segments of `seg` tokens (a multiple of kSsmBlock), nseg in all
   int seg, nseg;
   float* seg_state;     // workspace [nseg, D, N]: a segment's end from a zero start, then its start
   float* seg_sum;       // workspace [nseg, D]: the segment's summed step sizes

@@ -22,6 +22,8 @@ int check_dtype(int dtype) {
 int check_pitch(const char* name, const void* p, int64_t pitch, int width) {
   if (p && pitch < width)
     return fail(GDN_ERR_INVALID, "%s's pitch %lld is less than its row of %d", name, (long long)pitch, width);
+  if (p && pitch > GDN_MAX_PITCH)
+    return fail(GDN_ERR_UNSUPPORTED, "%s's pitch %lld exceeds %d", name, (long long)pitch, GDN_MAX_PITCH);
   return GDN_OK;
 }
 

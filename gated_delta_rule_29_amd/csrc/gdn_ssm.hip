@@ -9,7 +9,7 @@
 // holds 64 / LN channels.  Lane j of a channel also owns every LN-th token: it loads that token's x,
 // dt and z and forms its step size, gate and output once, and the channel's other lanes read the
 // two values they need through lane-exchange operands.  B and C, shared by all channels, are staged as
-// fp32 in LDS, 32 tokens at a time.  Everything is fp32 but the inputs' and outputs' own types.
+// fp32 in LDS, a block at a time.  Everything is fp32 but the inputs' and outputs' own types.
 //
 // Long sequences are cut into segments where there are too few channels to fill the chip: a first
 // kernel forms each segment's end state from a zero start, a second joins them (a segment's whole
@@ -21,86 +21,143 @@ namespace gdn {
 
 namespace {
 
-// SUMMARY: only the state from a zero start and the summed step sizes of a segment.
-template <typename T, int LN, int NPL, bool SUMMARY>
-__global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
-  constexpr int NP = LN * NPL, CH = 64 / LN, TL = kSsmChunk / LN;
-  __shared__ __align__(16) float bc[kSsmChunk * NP * 2];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int j = lane % LN, seg = blockIdx.x / groups;
-  const int c = ((blockIdx.x - seg * groups) * 4 + wv) * CH + lane / LN;
-  const bool cv = c < p.D;
-  const int cc = cv ? c : p.D - 1;  // loads of the lanes past the last channel stay inside
-  const Piece pc = find_piece(p.s, seg, p.seg, lane);
-  if (pc.seq < 0) return;
-  const int t0 = pc.begin + pc.k * p.seg, t1 = min(t0 + p.seg, pc.end);
-  if (SUMMARY && t1 == pc.end) return;  // nothing follows the last segment
-
-  float A2[NPL], h[NPL];
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int n = j * NPL + i;
-    A2[i] = n < p.N ? p.A[(int64_t)cc * p.N + n] * kLog2e : 0.f;
-  }
-  load_state<NPL>(SUMMARY ? nullptr : p.seg_state ? p.seg_state + (int64_t)seg * p.D * p.N
-                  : p.h0 ? p.h0 + (int64_t)pc.seq * p.D * p.N : nullptr, cc, j, p.N, h);
-  const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f, skip = p.skip ? p.skip[cc] : 0.f;
+// The state from a zero start and the summed step sizes of a segment.  No prefetch: eight waves a SIMD
+// hide the loads.
+template <typename T, int LN, int NPL>
+__global__ __launch_bounds__(256) void ssm_fwd_summary_kernel(SsmParams p, int groups) {
+  constexpr int NP = LN * NPL, TL = kSsmBlock / LN;
+  __shared__ __align__(16) float bc[kSsmBlock * NP * 2];
+  const Place<LN> w(p, groups);
+  if (w.pc.seq < 0 || w.t1 == w.pc.end) return;  // nothing follows the last segment
+  const int j = w.j, cc = w.cc;
+  float A2[NPL], h[NPL] = {};
+  load_decay<NPL>(p, cc, j, A2);
+  const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f;
   float dsum = 0.f;
-  int64_t chunk = 0;
-  if (!SUMMARY && p.h) chunk = find_piece_before(p.s, pc, kSsmChunk, lane) + (t0 - pc.begin) / kSsmChunk;
-
-  for (int tb = t0; tb < t1; tb += kSsmChunk) {
-    __syncthreads();
-    stage_bc<T, NP>(p, tb, t1, bc);
-    if (!SUMMARY && p.h) {
-      if (cv) store_state<NPL>(p.h + chunk * p.D * p.N, c, j, p.N, h);
-      ++chunk;
-    }
-    float xr[TL], dr[TL], zr[TL];
+  for (int tb = w.t0; tb < w.t1; tb += kSsmBlock) {  // (whole blocks: only a last segment ends inside one)
+    unsigned xr[TL], dr[TL];
+    StageBC<T, NP, kSsmBlock, 256> st;
+    const auto rx = window<T>(p.x, p.x_pitch, tb, kSsmBlock, p.D), rd = window<T>(p.dt, p.dt_pitch, tb, kSsmBlock, p.D);
 #pragma unroll
     for (int g = 0; g < TL; ++g) {
-      const int t = tb + g * LN + j;
-      const bool v = t < t1;
-      xr[g] = v ? to_f(static_cast<const T*>(p.x)[t * p.x_pitch + cc]) : 0.f;
-      dr[g] = v ? to_f(static_cast<const T*>(p.dt)[t * p.dt_pitch + cc]) : 0.f;
-      zr[g] = !SUMMARY && p.z && v ? to_f(static_cast<const T*>(p.z)[t * p.z_pitch + cc]) : 0.f;
+      xr[g] = load_bits<T>(rx, (unsigned)((g * LN + j) * (int)p.x_pitch + cc) * sizeof(T));
+      dr[g] = load_bits<T>(rd, (unsigned)((g * LN + j) * (int)p.dt_pitch + cc) * sizeof(T));
     }
+    st.load(p, tb, kSsmBlock);
+    __syncthreads();
+    st.store(bc);
     __syncthreads();
 #pragma unroll
     for (int g = 0; g < TL; ++g) {
-      const int t = tb + g * LN + j;
-      float de = dr[g] + bias;
-      if (p.softplus) de = softplus_f(de, nullptr);
-      if (t >= t1) de = 0.f;  // a token behind the end keeps the state as it is
-      const float dx = de * xr[g];
+      float de = of_bits<T>(dr[g]) + bias;
+      const float sp = softplus_f(de, nullptr);
+      de = p.softplus ? sp : de;
+      const float dx = de * of_bits<T>(xr[g]);
       dsum += de;
-      float yp[LN];
       static_for<LN>([&](auto k) {
         const float dk = lane_of<LN, k()>(de), xk = lane_of<LN, k()>(dx);
         float b[NPL], cf[NPL];
         read_bc<NPL>(bc + ((g * LN + k()) * NP + j * NPL) * 2, b, cf);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dk * A2[i]), h[i], xk * b[i]);
+      });
+      __builtin_amdgcn_sched_barrier(0);  // keeps the exponentials of later tokens from filling the registers
+    }
+  }
+  if (w.cv) store_state<NPL>(p.seg_state + (int64_t)w.seg * p.D * p.N, w.c, j, p.N, h);
+  dsum = group_sum<LN>(dsum);
+  if (w.cv && j == 0) p.seg_sum[(int64_t)w.seg * p.D + w.c] = dsum;
+}
+
+// A block's inputs are asked for while the block before it is computed, its B and C go to the other of two
+// LDS buffers, and outputs are stored at the block's end, so that the 32 tokens are one stretch of
+// code without branches.
+template <typename T, int LN, int NPL>
+__global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
+  constexpr int NP = LN * NPL, TL = kSsmBlock / LN;
+  __shared__ __align__(16) float bc[2][kSsmBlock * NP * 2];
+  const Place<LN> w(p, groups);
+  if (w.pc.seq < 0) return;
+  const int j = w.j, cc = w.cc, t1 = w.t1;
+
+  const bool gate = p.z;
+  const void* zp = gate ? p.z : p.x;
+  const int64_t zpitch = gate ? p.z_pitch : p.x_pitch;
+  const unsigned vx = (unsigned)(j * (int)p.x_pitch + cc) * sizeof(T), vd = (unsigned)(j * (int)p.dt_pitch + cc) * sizeof(T),
+                 vz = (unsigned)(j * (int)zpitch + cc) * sizeof(T);
+  unsigned xr[TL], dr[TL], zr[TL];
+  StageBC<T, NP, kSsmBlock, 256> st;
+  auto ask = [&](int tb) {
+    const int rows = min(t1 - tb, kSsmBlock);
+    const auto rx = window<T>(p.x, p.x_pitch, tb, rows, p.D), rd = window<T>(p.dt, p.dt_pitch, tb, rows, p.D),
+               rz = window<T>(zp, zpitch, tb, rows, p.D);
+#pragma unroll
+    for (int g = 0; g < TL; ++g) {
+      xr[g] = load_bits<T>(rx, vx + g * LN * (unsigned)p.x_pitch * sizeof(T));
+      dr[g] = load_bits<T>(rd, vd + g * LN * (unsigned)p.dt_pitch * sizeof(T));
+      zr[g] = load_bits<T>(rz, vz + g * LN * (unsigned)zpitch * sizeof(T));
+    }
+    st.load(p, tb, rows);
+  };
+  ask(w.t0);
+
+  const int64_t DN = (int64_t)p.D * p.N;
+  float A2[NPL], h[NPL];
+  load_decay<NPL>(p, cc, j, A2);
+  load_state<NPL>(p.seg_state ? p.seg_state + w.seg * DN : p.h0 ? p.h0 + w.pc.seq * DN : nullptr, cc, j, p.N, h);
+  const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f, skip = p.skip ? p.skip[cc] : 0.f;
+  float* save = nullptr;
+  if (p.h) save = p.h + (find_piece_before(p.s, w.pc, kSsmChunk, w.lane) + (w.t0 - w.pc.begin) / kSsmChunk) * DN;
+  const unsigned vy = w.cv ? (unsigned)(j * p.D + w.c) * sizeof(T) : kNowhere;
+  st.store(bc[0]);
+  __syncthreads();
+
+  int buf = 0;
+  for (int tb = w.t0; tb < t1; tb += kSsmBlock, buf ^= 1) {
+    float x[TL], z[TL], de[TL];
+#pragma unroll
+    for (int g = 0; g < TL; ++g) {
+      x[g] = of_bits<T>(xr[g]);
+      z[g] = of_bits<T>(zr[g]);
+      de[g] = of_bits<T>(dr[g]) + bias;
+    }
+    const bool more = tb + kSsmBlock < t1;
+    if (more) ask(tb + kSsmBlock);
+    const auto ry = window<T>(p.y, p.D, tb, min(t1 - tb, kSsmBlock), p.D);
+#pragma unroll
+    for (int g = 0; g < TL; ++g) {
+      if (save && g * LN % kSsmChunk == 0 && tb + g * LN < t1) {
+        if (w.cv) store_state<NPL>(save, w.c, j, p.N, h);
+        save += DN;
+      }
+      const float sp = softplus_f(de[g], nullptr);
+      de[g] = p.softplus ? sp : de[g];
+      if (tb + g * LN + j >= t1) de[g] = 0.f;  // a token behind the end keeps the state as it is
+      const float dx = de[g] * x[g];
+      float yp[LN];
+      static_for<LN>([&](auto k) {
+        const float dk = lane_of<LN, k()>(de[g]), xk = lane_of<LN, k()>(dx);
+        float b[NPL], cf[NPL];
+        read_bc<NPL>(bc[buf] + ((g * LN + k()) * NP + j * NPL) * 2, b, cf);
         float acc = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
           h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dk * A2[i]), h[i], xk * b[i]);
-          if (!SUMMARY) acc = __builtin_fmaf(cf[i], h[i], acc);
+          acc = __builtin_fmaf(cf[i], h[i], acc);
         }
         yp[k()] = acc;
       });
-      if (!SUMMARY) {
-        float y = reduce_scatter<LN>(yp, j) + skip * xr[g];
-        if (p.z) y *= zr[g] * sigmoid_f(zr[g]);
-        if (cv && t < t1) static_cast<T*>(p.y)[(int64_t)t * p.D + c] = to_t<T>(y);
-      }
+      float y = reduce_scatter<LN>(yp, j) + skip * x[g];
+      const float s = z[g] * sigmoid_f(z[g]);
+      y *= gate ? s : 1.f;
+      store_bits<T>(ry, to_t<T>(y), vy + g * LN * (unsigned)p.D * sizeof(T));  // dropped behind the end
+    }
+    if (more) {
+      st.store(bc[buf ^ 1]);  // read last before the barrier of the block before
+      __syncthreads();
     }
   }
-  if (SUMMARY) {
-    if (cv) store_state<NPL>(p.seg_state + (int64_t)seg * p.D * p.N, c, j, p.N, h);
-    dsum = group_sum<LN>(dsum);
-    if (cv && j == 0) p.seg_sum[(int64_t)seg * p.D + c] = dsum;
-  } else if (p.ht && t1 == pc.end && cv) {
-    store_state<NPL>(p.ht + (int64_t)pc.seq * p.D * p.N, c, j, p.N, h);
-  }
+  if (p.ht && t1 == w.pc.end && w.cv) store_state<NPL>(p.ht + w.pc.seq * DN, w.c, j, p.N, h);
 }
 
 // A sequence's segments in order: seg_state becomes the state at each segment's start.
@@ -172,12 +229,12 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmStepParams p, int grou
 int ssm_segment(bool backward, int rows, int nseq, int max_len, int D, int N) {
   const int ch = N <= 16 ? 16 : 4;  // channels of a wave
   const int64_t per_seg = (D + ch - 1) / ch;
-  const int round = (max_len + kSsmChunk - 1) / kSsmChunk * kSsmChunk;
-  if (per_seg * nseq >= 1024 || max_len <= 4 * kSsmChunk) return round;
-  const int64_t want = (2048 + per_seg - 1) / per_seg;  // segments in all
+  const int round = (max_len + kSsmBlock - 1) / kSsmBlock * kSsmBlock;
+  if (per_seg * nseq >= 2048 || max_len <= 4 * kSsmBlock) return round;
+  const int64_t want = (8192 + per_seg - 1) / per_seg;  // segments in all
   int64_t seg = (rows + want - 1) / want;
-  seg = (seg + kSsmChunk - 1) / kSsmChunk * kSsmChunk;
-  if (seg < 4 * kSsmChunk) seg = 4 * kSsmChunk;
+  seg = (seg + kSsmBlock - 1) / kSsmBlock * kSsmBlock;
+  if (seg < 4 * kSsmBlock) seg = 4 * kSsmBlock;
   return seg >= round ? round : (int)seg;
 }
 
@@ -194,13 +251,13 @@ hipError_t launch_ssm_fwd(SsmParams p, int dtype, void* ws, hipStream_t st) {
     const dim3 grid((unsigned)(groups * p.nseg));
     hipError_t e;
     if (split) {
-      ssm_fwd_kernel<T, LN, NPL, true><<<grid, 256, 0, st>>>(p, groups);
+      ssm_fwd_summary_kernel<T, LN, NPL><<<grid, 256, 0, st>>>(p, groups);
       if ((e = hipGetLastError()) != hipSuccess) return e;
       const int per_seq = (int)(((int64_t)p.D * p.N + 255) / 256);
       ssm_join_kernel<<<dim3((unsigned)(per_seq * p.s.n)), 256, 0, st>>>(p, per_seq);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    ssm_fwd_kernel<T, LN, NPL, false><<<grid, 256, 0, st>>>(p, groups);
+    ssm_fwd_kernel<T, LN, NPL><<<grid, 256, 0, st>>>(p, groups);
     return hipGetLastError();
   });
 }

@@ -41,17 +41,60 @@ __device__ __forceinline__ void store_state(float* st, int c, int j, int N, cons
   }
 }
 
-// B and C of the 32 tokens from tb on as fp32 pairs bc[token][n][B, C]; zero for n >= N and for tokens
-// behind t1.
-template <typename T, int NP>
-__device__ __forceinline__ void stage_bc(const SsmParams& p, int tb, int t1, float* bc) {
-  for (int e = threadIdx.x; e < kSsmChunk * NP; e += blockDim.x) {
-    const int tk = e / NP, n = e % NP, t = tb + tk;
-    const bool v = n < p.N && t < t1;
-    bc[2 * e] = v ? to_f(static_cast<const T*>(p.Bm)[t * p.b_pitch + n]) : 0.f;
-    bc[2 * e + 1] = v ? to_f(static_cast<const T*>(p.Cm)[t * p.c_pitch + n]) : 0.f;
-  }
+constexpr unsigned kNowhere = 0x80000000u;  // an offset behind the end of every buffer here
+
+// A buffer over `rows` rows of `width` elements from row `row` on: loads behind the last one give 0, so
+// that no load needs a branch (a branch around each load would have each waited for by itself).
+// row, rows and the pitch are the same in all lanes.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void* base, int64_t pitch, int row, int rows, int width) {
+  const T* p = static_cast<const T*>(base) + row * pitch;
+  const int bytes = rows > 0 ? (int)(((rows - 1) * pitch + width) * (int64_t)sizeof(T)) : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, bytes, 0x00020000);
 }
+// The element at byte offset off, as its bits.  (All of the offset is in the lane's part: the scalar
+// part of a buffer offset is not compared with the buffer's end.)
+template <typename T>
+__device__ __forceinline__ unsigned load_bits(__amdgpu_buffer_rsrc_t r, unsigned off) {
+  if constexpr (sizeof(T) == 2) return (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+  else return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+}
+// A store there; dropped behind the buffer's end.
+template <typename T>
+__device__ __forceinline__ void store_bits(__amdgpu_buffer_rsrc_t r, T v, unsigned off) {
+  if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, v), r, off, 0, 0);
+  else __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, v), r, off, 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ float of_bits(unsigned b) {
+  return __uint_as_float(sizeof(T) == 2 ? b << 16 : b);
+}
+
+// B and C of TOK tokens on their way to LDS: load() asks for them, store() writes them as fp32 pairs
+// bc[token][n][B, C], zero for n >= N and for tokens behind the end.
+template <typename T, int NP, int TOK, int THREADS>
+struct StageBC {
+  static constexpr int PER = (TOK * NP + THREADS - 1) / THREADS;
+  unsigned b[PER], c[PER];
+  __device__ __forceinline__ void load(const SsmParams& p, int tb, int rows) {
+    const auto rb = window<T>(p.Bm, p.b_pitch, tb, rows, p.N), rc = window<T>(p.Cm, p.c_pitch, tb, rows, p.N);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = i * THREADS + threadIdx.x, tk = e / NP, n = e % NP;
+      const bool v = n < p.N && tk < TOK;
+      b[i] = load_bits<T>(rb, v ? (unsigned)(tk * (int)p.b_pitch + n) * sizeof(T) : kNowhere);
+      c[i] = load_bits<T>(rc, v ? (unsigned)(tk * (int)p.c_pitch + n) * sizeof(T) : kNowhere);
+    }
+  }
+  __device__ __forceinline__ void store(float* bc) const {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = i * THREADS + threadIdx.x;
+      if (PER * THREADS == TOK * NP || e < TOK * NP)
+        *reinterpret_cast<float2*>(bc + 2 * e) = make_float2(of_bits<T>(b[i]), of_bits<T>(c[i]));
+    }
+  }
+};
 
 template <int NPL>
 __device__ __forceinline__ void read_bc(const float* q, float (&b)[NPL], float (&c)[NPL]) {
@@ -59,6 +102,16 @@ __device__ __forceinline__ void read_bc(const float* q, float (&b)[NPL], float (
   for (int i = 0; i < NPL; ++i) {
     b[i] = q[2 * i];
     c[i] = q[2 * i + 1];
+  }
+}
+
+// A channel's decay factors A log2(e) of a lane's states, zero behind the N-th.
+template <int NPL>
+__device__ __forceinline__ void load_decay(const SsmParams& p, int cc, int j, float (&A2)[NPL]) {
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int n = j * NPL + i;
+    A2[i] = n < p.N ? p.A[(int64_t)cc * p.N + n] * kLog2e : 0.f;
   }
 }
 
@@ -72,6 +125,16 @@ __device__ __forceinline__ float group_sum(float x) {
     x += dpp<kDppMirror>(x);
   }
   return x;
+}
+
+// The piece with its fields known to be the same in all lanes.
+__device__ __forceinline__ Piece uniform(Piece p) {
+  p.seq = __builtin_amdgcn_readfirstlane(p.seq);
+  p.k = __builtin_amdgcn_readfirstlane(p.k);
+  p.before = __builtin_amdgcn_readfirstlane(p.before);
+  p.begin = __builtin_amdgcn_readfirstlane(p.begin);
+  p.end = __builtin_amdgcn_readfirstlane(p.end);
+  return p;
 }
 
 // Pieces of `len` tokens before sequence pc.seq.
@@ -95,6 +158,29 @@ __device__ __forceinline__ SeqPieces pieces_of(const Seqs& s, int seq, int len, 
   r.count = (max(seq_begin(s, seq + 1) - seq_begin(s, seq), 0) + len - 1) / len;
   return r;
 }
+
+// What a workgroup of four waves does: a segment, 4 * 64 / LN channels of it, and this lane's part.
+template <int LN>
+struct Place {
+  static constexpr int CH = 64 / LN;
+  int lane, wv, j, seg, grp, c, cc, t0, t1;
+  bool cv;  // the lane has a channel (loads of a lane without one read the last channel's)
+  Piece pc;
+  __device__ __forceinline__ Place(const SsmParams& p, int groups) {
+    const int bid = xcd_contiguous(blockIdx.x, gridDim.x);
+    lane = threadIdx.x & 63;
+    wv = threadIdx.x >> 6;
+    j = lane % LN;
+    seg = bid / groups;
+    grp = bid - seg * groups;
+    c = (grp * 4 + wv) * CH + lane / LN;
+    cv = c < p.D;
+    cc = cv ? c : p.D - 1;
+    pc = uniform(find_piece(p.s, seg, p.seg, lane));
+    t0 = pc.begin + pc.k * p.seg;
+    t1 = min(t0 + p.seg, pc.end);
+  }
+};
 
 // f(T{}, LN, NPL) for these types and states: four lanes a channel up to 16 states, 16 beyond.
 template <typename F>

@@ -1,5 +1,5 @@
 // gdn_ssmbwd.hip -- gradient of the selective state space scan, from the states that the forward saved
-// every 32 tokens.
+// every 16 tokens.
 //
 // With y' the gradient of the ungated output (dy silu(z), or dy), a_t = e^{de_t A} and g_t the
 // gradient of h_t:
@@ -8,19 +8,17 @@
 //   dde_t = x_t (g_t . B_t) + sum_n A g_t a_t h_{t-1},   dA = sum_t de_t g_t a_t h_{t-1}
 //   ddt_t = dde_t softplus'(dt_t + dt_bias),   dz_t = dy_t y_t silu'(z_t),   dh0 = a_0 g_0
 //
-// Lanes as in the forward (gdn_ssm.hip).  A workgroup walks the 32-token chunks of its segment from
-// the last to the first: it forms the chunk's a_t h_{t-1} from the saved state into registers, then
-// walks the tokens backwards.  dB and dC are sums over all channels: each wave adds up its
-// channels' shares in registers, the workgroup its waves' in LDS, and a last kernel the workgroups'
-// in a fixed order.
+// Lanes as in the forward (gdn_ssm.hip).  A workgroup walks the 16-token chunks of its segment from
+// the last to the first: it forms the chunk's a_t and a_t h_{t-1} from the saved state into registers
+// (16 tokens of both are what they hold), then walks the tokens backwards.  dB and dC are sums
+// over all channels: each wave adds up its channels' shares through LDS, the workgroup its waves',
+// and a last kernel the workgroups', in a fixed order.
 #include "../../include/gdn.h"
 #include "gdn_ssm_device.h"
 
 namespace gdn {
 
 namespace {
-
-constexpr int kDppRor8 = 0x128, kDppQuadReverse = 0x1B;
 
 __device__ __forceinline__ float fold32(float a, float b) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
@@ -31,29 +29,81 @@ __device__ __forceinline__ float fold16(float a, float b) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Adds a lane's shares db[i], dc[i] of one token over the wave's channels and writes the sums to
-// out[2][NP] (dB, then dC).  Each exchange also halves the number of values: the lower half wave
-// goes on with dB, the upper with dC, then even and odd rows of 16 with even and odd i.
+// Adds the shares of dB and dC over a wave's channels.  put() takes a lane's shares of token k of a group
+// of LN tokens, done() leaves the group's sums in out[token][dB: NP, dC: NP].
+//
+// 16 lanes a channel (4 channels): by lane exchanges that halve the values too; the lower half
+// wave goes on with dB, the upper with dC, then even and odd rows of 16 lanes with even and odd i.
 template <int LN, int NPL>
-__device__ __forceinline__ void add_channels(const float (&db)[NPL], const float (&dc)[NPL], float* out, int lane) {
-  constexpr int NP = LN * NPL;
-  float u[NPL / 2];
+struct AddChannels {
+  static constexpr int NP = LN * NPL, LDS = 4;
+  float* out;
+  int lane;
+  __device__ __forceinline__ AddChannels(float*, int l) : lane(l) {}
+  __device__ __forceinline__ void put(int k, const float (&db)[NPL], const float (&dc)[NPL]) {
+    float* q = out + k * 2 * NP + (lane >> 5) * NP + (lane & 15) * NPL + ((lane >> 4) & 1);
 #pragma unroll
-  for (int i = 0; i < NPL / 2; ++i)
-    u[i] = fold16(fold32(db[2 * i], dc[2 * i]), fold32(db[2 * i + 1], dc[2 * i + 1]));
-  float* q = out + (lane >> 5) * NP;
-  const int odd = (lane >> 4) & 1;
-  if constexpr (LN == 16) {
-#pragma unroll
-    for (int i = 0; i < NPL / 2; ++i) q[(lane & 15) * NPL + 2 * i + odd] = u[i];
-  } else {
-    static_assert(LN == 4 && NPL == 4, "four lanes hold four states each");
-    const bool b3 = lane & 8;
-    float r = (b3 ? u[1] : u[0]) + dpp<kDppRor8>(b3 ? u[0] : u[1]);
-    r += dpp<kDppHalfMirror>(dpp<kDppQuadReverse>(r));  // lane ^ 4
-    if (!(lane & 4)) q[(lane & 3) * 4 + (b3 ? 2 : 0) + odd] = r;
+    for (int i = 0; i < NPL / 2; ++i)
+      q[2 * i] = fold16(fold32(db[2 * i], dc[2 * i]), fold32(db[2 * i + 1], dc[2 * i + 1]));
   }
-}
+  __device__ __forceinline__ void done() {}
+};
+// Four lanes a channel (16 channels): exchanges would cost as much as the gradient itself (17
+// instructions a token, half of them at a third of the rate), so the shares go through the
+// wave's own LDS: [token][dB, dC][channel][16], each lane then adds two columns of one token.
+template <>
+struct AddChannels<4, 4> {
+  static constexpr int WHICH = 16 * 16 + 16;  // padded: dB and dC of a token on different banks
+  static constexpr int LDS = 4 * 2 * WHICH;
+  float *buf, *out;
+  int lane;
+  __device__ __forceinline__ AddChannels(float* b, int l) : buf(b), lane(l) {}
+  __device__ __forceinline__ void put(int k, const float (&db)[4], const float (&dc)[4]) {
+    float* q = buf + k * 2 * WHICH + lane * 4;
+    *reinterpret_cast<f32x4*>(q) = f32x4{db[0], db[1], db[2], db[3]};
+    *reinterpret_cast<f32x4*>(q + WHICH) = f32x4{dc[0], dc[1], dc[2], dc[3]};
+  }
+  __device__ __forceinline__ void done() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int tok = lane >> 4, which = (lane >> 3) & 1, n = (lane & 7) * 2;
+    const float* q = buf + (tok * 2 + which) * WHICH + n;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float2 v = *reinterpret_cast<const float2*>(q + c * 16);
+      s0 += v.x;
+      s1 += v.y;
+    }
+    *reinterpret_cast<float2*>(out + tok * 32 + which * 16 + n) = make_float2(s0, s1);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+};
+
+// A chunk's x, dt, z and dy as a lane owns them: the j-th of every LN tokens of channel cc; 0 behind the
+// end.  (Without a gate z is read as x and not used.)
+template <typename T, int LN>
+struct ChunkIn {
+  static constexpr int TL = kSsmChunk / LN;
+  unsigned x[TL], dt[TL], z[TL], dy[TL];
+  __device__ __forceinline__ void ask(const SsmBwdParams& p, int tb, int t1, int j, int cc) {
+    const SsmParams& f = p.f;
+    const void* zp = f.z ? f.z : f.x;
+    const int64_t zpitch = f.z ? f.z_pitch : f.x_pitch;
+    const int rows = min(t1 - tb, kSsmChunk);
+    const auto rx = window<T>(f.x, f.x_pitch, tb, rows, f.D), rd = window<T>(f.dt, f.dt_pitch, tb, rows, f.D),
+               rz = window<T>(zp, zpitch, tb, rows, f.D), ry = window<T>(p.dy, p.dy_pitch, tb, rows, f.D);
+    auto at = [&](int64_t pitch) { return (unsigned)(j * (int)pitch + cc) * (unsigned)sizeof(T); };
+    const unsigned vx = at(f.x_pitch), vd = at(f.dt_pitch), vz = at(zpitch), vy = at(p.dy_pitch);
+#pragma unroll
+    for (int q = 0; q < TL; ++q) {
+      const unsigned s = q * LN * sizeof(T);
+      x[q] = load_bits<T>(rx, vx + s * (unsigned)f.x_pitch);
+      dt[q] = load_bits<T>(rd, vd + s * (unsigned)f.dt_pitch);
+      z[q] = load_bits<T>(rz, vz + s * (unsigned)zpitch);
+      dy[q] = load_bits<T>(ry, vy + s * (unsigned)p.dy_pitch);
+    }
+  }
+};
 
 // A token's step size, its derivative by the raw one, and the gradient of the ungated output.
 struct Token {
@@ -61,67 +111,55 @@ struct Token {
 };
 __device__ __forceinline__ Token token_of(bool v, bool softplus, bool gate, float raw, float dout, float z) {
   Token k;
-  k.de = raw;
-  k.sig = 1.f;
-  if (softplus) k.de = softplus_f(raw, &k.sig);
-  if (!v) k.de = 0.f;
-  k.gy = gate ? dout * z * sigmoid_f(z) : dout;
+  float sig;
+  const float sp = softplus_f(raw, &sig), s = z * sigmoid_f(z);
+  k.de = v ? (softplus ? sp : raw) : 0.f;
+  k.sig = softplus ? sig : 1.f;
+  k.gy = dout * (gate ? s : 1.f);
   return k;
 }
 
 // Gradient of the state before a segment from its own tokens alone, and its summed step sizes.
 template <typename T, int LN, int NPL>
 __global__ __launch_bounds__(256) void ssm_bwd_summary_kernel(SsmBwdParams p, int groups) {
-  constexpr int NP = LN * NPL, CH = 64 / LN, TL = kSsmChunk / LN;
+  constexpr int NP = LN * NPL, TL = kSsmChunk / LN;
   __shared__ __align__(16) float bc[kSsmChunk * NP * 2];
   const SsmParams& f = p.f;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int j = lane % LN, seg = blockIdx.x / groups;
-  const int c = ((blockIdx.x - seg * groups) * 4 + wv) * CH + lane / LN;
-  const bool cv = c < f.D;
-  const int cc = cv ? c : f.D - 1;
-  const Piece pc = find_piece(f.s, seg, f.seg, lane);
-  if (pc.seq < 0 || pc.k == 0) return;  // nothing is before the first segment
-  const int t0 = pc.begin + pc.k * f.seg, t1 = min(t0 + f.seg, pc.end);
+  const Place<LN> w(f, groups);
+  if (w.pc.seq < 0 || w.pc.k == 0) return;  // nothing is before the first segment
+  const int j = w.j, cc = w.cc, t0 = w.t0, t1 = w.t1;
   float A2[NPL], g[NPL] = {};
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int n = j * NPL + i;
-    A2[i] = n < f.N ? f.A[(int64_t)cc * f.N + n] * kLog2e : 0.f;
-  }
+  load_decay<NPL>(f, cc, j, A2);
   const float bias = f.dt_bias ? f.dt_bias[cc] : 0.f;
   float dsum = 0.f;
   for (int tb = t0 + (t1 - t0 - 1) / kSsmChunk * kSsmChunk; tb >= t0; tb -= kSsmChunk) {
+    ChunkIn<T, LN> in;
+    StageBC<T, NP, kSsmChunk, 256> st;
+    in.ask(p, tb, t1, j, cc);
+    st.load(f, tb, min(t1 - tb, kSsmChunk));
     __syncthreads();
-    stage_bc<T, NP>(f, tb, t1, bc);
-    Token tk[TL];
-#pragma unroll
-    for (int q = 0; q < TL; ++q) {
-      const int t = tb + q * LN + j;
-      const bool v = t < t1;
-      const float raw = (v ? to_f(static_cast<const T*>(f.dt)[t * f.dt_pitch + cc]) : 0.f) + bias;
-      const float dout = v ? to_f(static_cast<const T*>(p.dy)[t * p.dy_pitch + cc]) : 0.f;
-      const float z = f.z && v ? to_f(static_cast<const T*>(f.z)[t * f.z_pitch + cc]) : 0.f;
-      tk[q] = token_of(v, f.softplus, f.z != nullptr, raw, dout, z);
-      dsum += tk[q].de;
-    }
+    st.store(bc);
     __syncthreads();
 #pragma unroll
     for (int q = TL - 1; q >= 0; --q) {
+      const Token tk = token_of(tb + q * LN + j < t1, f.softplus, f.z != nullptr, of_bits<T>(in.dt[q]) + bias,
+                                of_bits<T>(in.dy[q]), of_bits<T>(in.z[q]));
+      dsum += tk.de;
       static_for<LN>([&](auto r) {
         constexpr int k = LN - 1 - r();
-        const float dk = lane_of<LN, k>(tk[q].de), gk = lane_of<LN, k>(tk[q].gy);
+        const float dk = lane_of<LN, k>(tk.de), gk = lane_of<LN, k>(tk.gy);
         float b[NPL], cf[NPL];
         read_bc<NPL>(bc + ((q * LN + k) * NP + j * NPL) * 2, b, cf);
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
           g[i] = __builtin_fmaf(cf[i], gk, g[i]) * __builtin_amdgcn_exp2f(dk * A2[i]);
       });
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
-  if (cv) store_state<NPL>(f.seg_state + (int64_t)seg * f.D * f.N, c, j, f.N, g);
+  if (w.cv) store_state<NPL>(f.seg_state + (int64_t)w.seg * f.D * f.N, w.c, j, f.N, g);
   dsum = group_sum<LN>(dsum);
-  if (cv && j == 0) f.seg_sum[(int64_t)seg * f.D + c] = dsum;
+  if (w.cv && j == 0) f.seg_sum[(int64_t)w.seg * f.D + w.c] = dsum;
 }
 
 // A sequence's segments from the last to the first: seg_state becomes the gradient that reaches each
@@ -146,122 +184,131 @@ __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(SsmBwdParams p, int p
 
 template <typename T, int LN, int NPL>
 __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int groups) {
-  constexpr int NP = LN * NPL, CH = 64 / LN, TL = kSsmChunk / LN;
-  __shared__ __align__(16) float bc[kSsmChunk * NP * 2];
-  __shared__ __align__(16) float red[4][kSsmChunk][2 * NP];
+  constexpr int NP = LN * NPL, TL = kSsmChunk / LN;
+  __shared__ __align__(16) float bc[2][kSsmChunk * NP * 2];
+  __shared__ __align__(16) float red[4][kSsmChunk * 2 * NP];
+  __shared__ __align__(16) float shares[4][AddChannels<LN, NPL>::LDS];
   const SsmParams& f = p.f;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int j = lane % LN, seg = blockIdx.x / groups, grp = blockIdx.x - seg * groups;
-  const int c = (grp * 4 + wv) * CH + lane / LN;
-  const bool cv = c < f.D;
-  const int cc = cv ? c : f.D - 1;
-  const Piece pc = find_piece(f.s, seg, f.seg, lane);
-  if (pc.seq < 0) return;
-  const int t0 = pc.begin + pc.k * f.seg, t1 = min(t0 + f.seg, pc.end);
+  const Place<LN> w(f, groups);
+  if (w.pc.seq < 0) return;
+  const int j = w.j, c = w.c, cc = w.cc, t0 = w.t0, t1 = w.t1;
+  const bool cv = w.cv, gate = f.z;
   const int64_t DN = (int64_t)f.D * f.N;
-  const int64_t chunk0 = find_piece_before(f.s, pc, kSsmChunk, lane) + (t0 - pc.begin) / kSsmChunk;
+  int tb = t0 + (t1 - t0 - 1) / kSsmChunk * kSsmChunk;
+
+  // a chunk's inputs are asked for while the one behind it is computed
+  ChunkIn<T, LN> in;
+  StageBC<T, NP, kSsmChunk, 256> st;
+  float hs[NPL];
+  const float* saved = f.h + (find_piece_before(f.s, w.pc, kSsmChunk, w.lane) + (tb - w.pc.begin) / kSsmChunk) * DN;
+  in.ask(p, tb, t1, j, cc);
+  st.load(f, tb, min(t1 - tb, kSsmChunk));
+  load_state<NPL>(saved, cc, j, f.N, hs);
 
   float A2[NPL], g[NPL], dA[NPL] = {};
+  load_decay<NPL>(f, cc, j, A2);
+  load_state<NPL>(f.seg_state ? f.seg_state + w.seg * DN : p.dht ? p.dht + w.pc.seq * DN : nullptr, cc, j, f.N, g);
+  if (!cv) {  // lanes without a channel give nothing to the sums over channels
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int n = j * NPL + i;
-    A2[i] = n < f.N ? f.A[(int64_t)cc * f.N + n] * kLog2e : 0.f;
+    for (int i = 0; i < NPL; ++i) g[i] = 0.f;
   }
-  load_state<NPL>(f.seg_state ? f.seg_state + seg * DN : p.dht ? p.dht + pc.seq * DN : nullptr, cc, j, f.N, g);
   const float bias = f.dt_bias ? f.dt_bias[cc] : 0.f, skip = f.skip ? f.skip[cc] : 0.f;
   float dskip = 0.f, dbias = 0.f;
+  const unsigned vo = cv ? (unsigned)(j * f.D + c) * sizeof(T) : kNowhere;
+  AddChannels<LN, NPL> add(shares[w.wv], w.lane);
+  st.store(bc[0]);
+  __syncthreads();
 
-  for (int tb = t0 + (t1 - t0 - 1) / kSsmChunk * kSsmChunk; tb >= t0; tb -= kSsmChunk) {
-    __syncthreads();
-    stage_bc<T, NP>(f, tb, t1, bc);
-    float h[NPL], ph[kSsmChunk][NPL];
-    load_state<NPL>(f.h + (chunk0 + (tb - t0) / kSsmChunk) * DN, cc, j, f.N, h);
-    float x[TL], z[TL], dout[TL];
+  for (int buf = 0; tb >= t0; tb -= kSsmChunk, buf ^= 1) {
+    float h[NPL], a[kSsmChunk][NPL], ah[kSsmChunk][NPL], x[TL], z[TL], dout[TL];
     Token tk[TL];
 #pragma unroll
-    for (int q = 0; q < TL; ++q) {
-      const int t = tb + q * LN + j;
-      const bool v = t < t1;
-      x[q] = v ? to_f(static_cast<const T*>(f.x)[t * f.x_pitch + cc]) : 0.f;
-      const float raw = (v ? to_f(static_cast<const T*>(f.dt)[t * f.dt_pitch + cc]) : 0.f) + bias;
-      dout[q] = v && cv ? to_f(static_cast<const T*>(p.dy)[t * p.dy_pitch + cc]) : 0.f;
-      z[q] = f.z && v ? to_f(static_cast<const T*>(f.z)[t * f.z_pitch + cc]) : 0.f;
-      tk[q] = token_of(v, f.softplus, f.z != nullptr, raw, dout[q], z[q]);
-    }
-    if (!cv) {  // lanes past the last channel give nothing to the sums over channels
+    for (int i = 0; i < NPL; ++i) h[i] = hs[i];
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) g[i] = 0.f;
+    for (int q = 0; q < TL; ++q) {
+      x[q] = of_bits<T>(in.x[q]);
+      z[q] = of_bits<T>(in.z[q]);
+      dout[q] = cv ? of_bits<T>(in.dy[q]) : 0.f;
+      tk[q] = token_of(tb + q * LN + j < t1, f.softplus, gate, of_bits<T>(in.dt[q]) + bias, dout[q], z[q]);
     }
-    __syncthreads();
+    const bool more = tb > t0;
+    if (more) {
+      saved -= DN;
+      in.ask(p, tb - kSsmChunk, t1, j, cc);
+      st.load(f, tb - kSsmChunk, kSsmChunk);
+      load_state<NPL>(saved, cc, j, f.N, hs);
+    }
 #pragma unroll
     for (int q = 0; q < TL; ++q) {
       const float dx = tk[q].de * x[q];
       static_for<LN>([&](auto k) {
         const float dk = lane_of<LN, k()>(tk[q].de), xk = lane_of<LN, k()>(dx);
         float b[NPL], cf[NPL];
-        read_bc<NPL>(bc + ((q * LN + k()) * NP + j * NPL) * 2, b, cf);
+        read_bc<NPL>(bc[buf] + ((q * LN + k()) * NP + j * NPL) * 2, b, cf);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-          const float ah = __builtin_amdgcn_exp2f(dk * A2[i]) * h[i];
-          ph[q * LN + k()][i] = ah;
-          h[i] = __builtin_fmaf(xk, b[i], ah);
+          const float e = __builtin_amdgcn_exp2f(dk * A2[i]);
+          a[q * LN + k()][i] = e;
+          ah[q * LN + k()][i] = e * h[i];
+          h[i] = __builtin_fmaf(xk, b[i], e * h[i]);
         }
       });
     }
+    const int rows = min(t1 - tb, kSsmChunk);
+    const auto rx = window<T>(p.dx, f.D, tb, rows, f.D), rd = window<T>(p.ddt, f.D, tb, rows, f.D),
+               rz = window<T>(gate ? p.dz : p.dx, f.D, tb, gate ? rows : 0, f.D);
 #pragma unroll
     for (int q = TL - 1; q >= 0; --q) {
       const float dx = tk[q].de * x[q];
       float yv[LN], gb[LN], ga[LN];
+      add.out = red[w.wv] + q * LN * 2 * NP;
       static_for<LN>([&](auto r) {
         constexpr int k = LN - 1 - r();
         const float dk = lane_of<LN, k>(tk[q].de), xk = lane_of<LN, k>(dx), gk = lane_of<LN, k>(tk[q].gy);
         float b[NPL], cf[NPL], db[NPL], dc[NPL];
-        read_bc<NPL>(bc + ((q * LN + k) * NP + j * NPL) * 2, b, cf);
+        read_bc<NPL>(bc[buf] + ((q * LN + k) * NP + j * NPL) * 2, b, cf);
         float sy = 0.f, sb = 0.f, sa = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-          const float ah = ph[q * LN + k][i], ht = __builtin_fmaf(xk, b[i], ah);
+          const float p_ = ah[q * LN + k][i], ht = __builtin_fmaf(xk, b[i], p_);
           sy = __builtin_fmaf(cf[i], ht, sy);
           g[i] = __builtin_fmaf(cf[i], gk, g[i]);
           dc[i] = gk * ht;
           db[i] = xk * g[i];
           sb = __builtin_fmaf(g[i], b[i], sb);
-          const float gah = g[i] * ah;
+          const float gah = g[i] * p_;
           sa = __builtin_fmaf(gah, A2[i], sa);
           dA[i] = __builtin_fmaf(gah, dk, dA[i]);
-          g[i] *= __builtin_amdgcn_exp2f(dk * A2[i]);
+          g[i] *= a[q * LN + k][i];
         }
         yv[k] = sy;
         gb[k] = sb;
         ga[k] = sa;
-        add_channels<LN, NPL>(db, dc, red[wv][q * LN + k], lane);
+        add.put(k, db, dc);
       });
+      add.done();
       const float y = reduce_scatter<LN>(yv, j), sb = reduce_scatter<LN>(gb, j), sa = reduce_scatter<LN>(ga, j);
-      const int t = tb + q * LN + j;
-      const float ddt = (x[q] * sb + sa * kLn2) * tk[q].sig;
-      if (t < t1 && cv) {
-        const int64_t o = (int64_t)t * f.D + c;
-        static_cast<T*>(p.dx)[o] = to_t<T>(tk[q].de * sb + skip * tk[q].gy);
-        static_cast<T*>(p.ddt)[o] = to_t<T>(ddt);
-        if (f.z) {
-          const float s = sigmoid_f(z[q]);
-          static_cast<T*>(p.dz)[o] = to_t<T>(dout[q] * (y + skip * x[q]) * s * (1.f + z[q] * (1.f - s)));
-        }
-        dbias += ddt;
-        dskip = __builtin_fmaf(tk[q].gy, x[q], dskip);
-      }
+      const float ddt = (x[q] * sb + sa * kLn2) * tk[q].sig, s = sigmoid_f(z[q]);
+      const unsigned so = q * LN * (unsigned)f.D * sizeof(T);  // stores behind the end are dropped
+      store_bits<T>(rx, to_t<T>(tk[q].de * sb + skip * tk[q].gy), vo + so);
+      store_bits<T>(rd, to_t<T>(ddt), vo + so);
+      store_bits<T>(rz, to_t<T>(dout[q] * (y + skip * x[q]) * s * (1.f + z[q] * (1.f - s))), vo + so);
+      dbias += tb + q * LN + j < t1 ? ddt : 0.f;
+      dskip = __builtin_fmaf(tk[q].gy, x[q], dskip);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    if (more) st.store(bc[buf ^ 1]);
     __syncthreads();
     for (int e = threadIdx.x; e < kSsmChunk * 2 * NP; e += 256) {
-      const int tk_ = e / (2 * NP), m = e % (2 * NP), n = m % NP, t = tb + tk_;
-      if (t < t1 && n < f.N) {
-        const float s = red[0][tk_][m] + red[1][tk_][m] + red[2][tk_][m] + red[3][tk_][m];
-        p.part_bc[(((int64_t)grp * f.s.rows + t) * 2 + m / NP) * f.N + n] = s;
-      }
+      const int k = e / (2 * NP), m = e % (2 * NP), n = m % NP;
+      if (k < rows && n < f.N)
+        p.part_bc[(((int64_t)w.grp * f.s.rows + tb + k) * 2 + m / NP) * f.N + n] =
+            red[0][e] + red[1][e] + red[2][e] + red[3][e];
     }
+    __syncthreads();
   }
   if (cv) {
-    float* pa = p.part_a + ((int64_t)seg * f.D + c) * (f.N + 2);
+    float* pa = p.part_a + ((int64_t)w.seg * f.D + c) * (f.N + 2);
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
       if (j * NPL + i < f.N) pa[j * NPL + i] = dA[i];
@@ -271,7 +318,7 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
       pa[f.N] = dskip;
       pa[f.N + 1] = dbias;
     }
-    if (p.dh0 && pc.k == 0) store_state<NPL>(p.dh0 + pc.seq * DN, c, j, f.N, g);
+    if (p.dh0 && w.pc.k == 0) store_state<NPL>(p.dh0 + w.pc.seq * DN, c, j, f.N, g);
   }
 }
 

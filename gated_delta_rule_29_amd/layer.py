@@ -16,7 +16,7 @@ __all__ = ["causal_conv_fwd", "causal_conv_fwd_varlen", "causal_conv_bwd", "caus
            "causal_conv_step", "ssm_scan_fwd", "ssm_scan_fwd_varlen", "ssm_scan_bwd", "ssm_scan_bwd_varlen",
            "ssm_step", "rms_norm_fwd", "rms_norm_q8_fwd", "rms_norm_bwd", "SSM_CHUNK"]
 
-SSM_CHUNK = 32
+SSM_CHUNK = 16
 F32 = torch.float32
 _DT = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16}
 

@@ -80,6 +80,8 @@ extern "C" {
 #define GDN_ERR_WORKSPACE 3   /* workspace missing or smaller than the size query returns   */
 #define GDN_ERR_HIP 4         /* a HIP launch or runtime call failed (RuntimeError)          */
 
+#define GDN_MAX_PITCH (1 << 23) /* elements from row to row of the layer operators' inputs */
+
 #define GDN_DTYPE_F32 0
 #define GDN_DTYPE_BF16 1
 
@@ -632,7 +634,8 @@ GDN_API int gdn_bwd_dhu_varlen(const void* q, const void* k, const void* w, cons
  *  - x [tokens, C] with a pitch: row r starts at x + r * pitch elements.  A dense batch of B
  *    sequences of T tokens has rows b * T + t; a packed batch (_varlen) has T_total rows,
  *    sequence i covering rows [cu[i], cu[i+1]), with cu_seqlens and cu_seqlens_host as in
- *    gdn_fwd_varlen.  Outputs are dense.
+ *    gdn_fwd_varlen.  Outputs are dense.  Pitches beyond GDN_MAX_PITCH are
+ *    GDN_ERR_UNSUPPORTED (32 rows are addressed with 32-bit offsets).
  *  - dtype is that of the activations (inputs and outputs that are not said to be fp32);
  *    all arithmetic, states and sums over tokens or channels are fp32, each result rounded once.
  *  - Pointers have their type's alignment; 16-byte alignment (and pitches and widths that are
@@ -712,7 +715,7 @@ GDN_API int causal_conv_step(const void* x, int64_t x_pitch, const float* w, con
  * joined by their states; results then differ from the uncut order in fp32 rounding only.
  * Supported: 1 <= N <= 64 (GDN_ERR_UNSUPPORTED otherwise), any D and T >= 1.
  */
-#define GDN_SSM_CHUNK 32
+#define GDN_SSM_CHUNK 16
 GDN_API size_t ssm_scan_fwd_workspace_bytes(int B, int T, int D, int N);
 GDN_API int ssm_scan_fwd(const void* x, int64_t x_pitch, const void* dt, int64_t dt_pitch,
                          const float* A, const void* Bm, int64_t b_pitch, const void* Cm,
