@@ -85,11 +85,10 @@ template <typename T, int LN>
 struct ChunkIn {
   static constexpr int TL = kSsmChunk / LN;
   unsigned x[TL], dt[TL], z[TL], dy[TL];
-  __device__ __forceinline__ void ask(const SsmBwdParams& p, int tb, int t1, int j, int cc) {
+  __device__ __forceinline__ void ask(const SsmBwdParams& p, int tb, int rows, int j, int cc) {
     const SsmParams& f = p.f;
     const void* zp = f.z ? f.z : f.x;
     const int64_t zpitch = f.z ? f.z_pitch : f.x_pitch;
-    const int rows = min(t1 - tb, kSsmChunk);
     const auto rx = window<T>(f.x, f.x_pitch, tb, rows, f.D), rd = window<T>(f.dt, f.dt_pitch, tb, rows, f.D),
                rz = window<T>(zp, zpitch, tb, rows, f.D), ry = window<T>(p.dy, p.dy_pitch, tb, rows, f.D);
     auto at = [&](int64_t pitch) { return (unsigned)(j * (int)pitch + cc) * (unsigned)sizeof(T); };
@@ -135,8 +134,9 @@ __global__ __launch_bounds__(256) void ssm_bwd_summary_kernel(SsmBwdParams p, in
   for (int tb = t0 + (t1 - t0 - 1) / kSsmChunk * kSsmChunk; tb >= t0; tb -= kSsmChunk) {
     ChunkIn<T, LN> in;
     StageBC<T, NP, kSsmChunk, 256> st;
-    in.ask(p, tb, t1, j, cc);
-    st.load(f, tb, min(t1 - tb, kSsmChunk));
+    const int rows = min(t1 - tb, kSsmChunk);
+    in.ask(p, tb, rows, j, cc);
+    st.load(f, tb, rows);
     __syncthreads();
     st.store(bc);
     __syncthreads();
@@ -186,7 +186,7 @@ template <typename T, int LN, int NPL>
 __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int groups) {
   constexpr int NP = LN * NPL, TL = kSsmChunk / LN;
   __shared__ __align__(16) float bc[2][kSsmChunk * NP * 2];
-  __shared__ __align__(16) float red[4][kSsmChunk * 2 * NP];
+  __shared__ __align__(16) float red[2][4][kSsmChunk * 2 * NP];
   __shared__ __align__(16) float shares[4][AddChannels<LN, NPL>::LDS];
   const SsmParams& f = p.f;
   const Place<LN> w(f, groups);
@@ -201,7 +201,7 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
   StageBC<T, NP, kSsmChunk, 256> st;
   float hs[NPL];
   const float* saved = f.h + (find_piece_before(f.s, w.pc, kSsmChunk, w.lane) + (tb - w.pc.begin) / kSsmChunk) * DN;
-  in.ask(p, tb, t1, j, cc);
+  in.ask(p, tb, min(t1 - tb, kSsmChunk), j, cc);
   st.load(f, tb, min(t1 - tb, kSsmChunk));
   load_state<NPL>(saved, cc, j, f.N, hs);
 
@@ -232,12 +232,6 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
       tk[q] = token_of(tb + q * LN + j < t1, f.softplus, gate, of_bits<T>(in.dt[q]) + bias, dout[q], z[q]);
     }
     const bool more = tb > t0;
-    if (more) {
-      saved -= DN;
-      in.ask(p, tb - kSsmChunk, t1, j, cc);
-      st.load(f, tb - kSsmChunk, kSsmChunk);
-      load_state<NPL>(saved, cc, j, f.N, hs);
-    }
 #pragma unroll
     for (int q = 0; q < TL; ++q) {
       const float dx = tk[q].de * x[q];
@@ -259,9 +253,16 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
                rz = window<T>(gate ? p.dz : p.dx, f.D, tb, gate ? rows : 0, f.D);
 #pragma unroll
     for (int q = TL - 1; q >= 0; --q) {
+      if (q == (TL > 1 ? TL - 2 : 0)) {  // the next chunk's inputs, once the last group's a and a h are done with
+        const int left = more ? kSsmChunk : 0;
+        saved -= more ? DN : 0;
+        in.ask(p, tb - kSsmChunk, left, j, cc);
+        st.load(f, tb - kSsmChunk, left);
+        load_state<NPL>(saved, cc, j, f.N, hs);
+      }
       const float dx = tk[q].de * x[q];
       float yv[LN], gb[LN], ga[LN];
-      add.out = red[w.wv] + q * LN * 2 * NP;
+      add.out = red[buf][w.wv] + q * LN * 2 * NP;
       static_for<LN>([&](auto r) {
         constexpr int k = LN - 1 - r();
         const float dk = lane_of<LN, k>(tk[q].de), xk = lane_of<LN, k>(dx), gk = lane_of<LN, k>(tk[q].gy);
@@ -286,7 +287,6 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
         ga[k] = sa;
         add.put(k, db, dc);
       });
-      add.done();
       const float y = reduce_scatter<LN>(yv, j), sb = reduce_scatter<LN>(gb, j), sa = reduce_scatter<LN>(ga, j);
       const float ddt = (x[q] * sb + sa * kLn2) * tk[q].sig, s = sigmoid_f(z[q]);
       const unsigned so = q * LN * (unsigned)f.D * sizeof(T);  // stores behind the end are dropped
@@ -295,17 +295,17 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
       store_bits<T>(rz, to_t<T>(dout[q] * (y + skip * x[q]) * s * (1.f + z[q] * (1.f - s))), vo + so);
       dbias += tb + q * LN + j < t1 ? ddt : 0.f;
       dskip = __builtin_fmaf(tk[q].gy, x[q], dskip);
-      __builtin_amdgcn_sched_barrier(0);
+      add.done();
     }
     if (more) st.store(bc[buf ^ 1]);
+    // one barrier a chunk: what is read here is written again two chunks on
     __syncthreads();
     for (int e = threadIdx.x; e < kSsmChunk * 2 * NP; e += 256) {
       const int k = e / (2 * NP), m = e % (2 * NP), n = m % NP;
       if (k < rows && n < f.N)
         p.part_bc[(((int64_t)w.grp * f.s.rows + tb + k) * 2 + m / NP) * f.N + n] =
-            red[0][e] + red[1][e] + red[2][e] + red[3][e];
+            red[buf][0][e] + red[buf][1][e] + red[buf][2][e] + red[buf][3][e];
     }
-    __syncthreads();
   }
   if (cv) {
     float* pa = p.part_a + ((int64_t)w.seg * f.D + c) * (f.N + 2);
