@@ -12,8 +12,18 @@ namespace gdn {
 
 namespace {
 
-// One thread walks the tokens of a tile for V channels (one 16-byte vector, or one channel where
-// widths, pitches or addresses do not allow that), its window in registers.
+// Both passes are bound by memory (2 or 3 values a token and channel, some 10 operations each).  One
+// thread walks the tokens of a tile for V channels, its window in registers; neighbouring threads have
+// neighbouring channels, so that a wave reads a row in one stretch.  V is 4 (one access of 8 or 16
+// bytes), or 1 where widths, pitches or addresses do not allow that.  Eight bf16 channels a thread
+// were slower: their taps, window and tokens take 150 registers (forward over 16384 x 4096 bf16
+// with a 32-token tile 64 us against 53, which is 5.1 TB/s; gradient 100 against 90).
+//
+// Tokens whose loads are asked for together; they have to hide the memory's latency.  (Forward with
+// 4: 61 us.  The gradient's other registers leave room for 4: 90 us against 104 with 8.)
+constexpr int kFwdBatch = 8, kBwdBatch = 4;
+constexpr int kBwdTile = 64;  // (the first tokens' window and the last ones' du are read twice)
+
 template <typename T, int W, int V>
 struct Filter {
   float w[W][V], b[V];
@@ -82,15 +92,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int groups,
   int begin = min(seq_begin(p.s, seq), t0), end = seq_begin(p.s, seq + 1);
   float win[W - 1][V];
   load_window<T, W, V>(p, seq, begin, t0, d0, win);
-  for (int t = t0; t < t1; ++t) {
-    if (t >= end && seq + 1 < p.s.n) {
-      ++seq;
-      begin = end;
-      end = seq_begin(p.s, seq + 1);
-      load_window<T, W, V>(p, seq, t, t, d0, win);
-    }
-    float xt[V], o[V];
-    loadv<T, V>(x + t * p.x_pitch + d0, xt);
+  auto token = [&](int t, const float (&xt)[V]) {
+    float o[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float u = f.u(win, xt, v);
@@ -98,7 +101,28 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int groups,
     }
     storev<T, V>(y + (int64_t)t * p.D + d0, o);
     shift<W, V>(win, xt);
-    if (p.last && t == end - 1) {
+  };
+  for (int t = t0; t < t1;) {
+    if (t >= end && seq + 1 < p.s.n) {
+      ++seq;
+      begin = end;
+      end = seq_begin(p.s, seq + 1);
+      load_window<T, W, V>(p, seq, t, t, d0, win);
+    }
+    if (t + kFwdBatch <= min(end, t1)) {
+      float xt[kFwdBatch][V];
+#pragma unroll
+      for (int i = 0; i < kFwdBatch; ++i) loadv<T, V>(x + (t + i) * p.x_pitch + d0, xt[i]);
+#pragma unroll
+      for (int i = 0; i < kFwdBatch; ++i) token(t + i, xt[i]);
+      t += kFwdBatch;
+    } else {
+      float xt[V];
+      loadv<T, V>(x + t * p.x_pitch + d0, xt);
+      token(t, xt);
+      ++t;
+    }
+    if (p.last && t == end) {
 #pragma unroll
       for (int k = 0; k < W - 1; ++k)
         storev<T, V>(static_cast<T*>(p.last) + ((int64_t)seq * (W - 1) + k) * p.D + d0, win[k]);
@@ -136,18 +160,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdParams p, int grou
     }
   };
 
-  for (int t = t0; t < t1 + W - 1; ++t) {
-    if (t >= end) {
-      if (t >= t1 || seq + 1 >= f.s.n) break;
-      ++seq;
-      begin = end;
-      end = seq_begin(f.s, seq + 1);
-      load_window<T, W, V>(f, seq, t, t, d0, win);
-    }
-    float xt[V], g[V];
-    loadv<T, V>(x + t * f.x_pitch + d0, xt);
-    loadv<T, V>(dy + t * p.dy_pitch + d0, g);
-    const bool mine = t < t1;
+  // mine: the token is the tile's own (its du counts in dw and dbias)
+  auto token = [&](int t, const float (&xt)[V], const float (&g)[V], bool mine) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float du = g[v];
@@ -171,7 +185,35 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdParams p, int grou
       for (int k = 0; k < W - 1; ++k) acc[k][v] = acc[k + 1][v];
       acc[W - 1][v] = 0.f;
     }
-    if (t == end - 1) {  // acc[k] is row end - (W-1) + k
+    shift<W, V>(win, xt);
+  };
+
+  for (int t = t0; t < t1 + W - 1;) {
+    if (t >= end) {
+      if (t >= t1 || seq + 1 >= f.s.n) break;
+      ++seq;
+      begin = end;
+      end = seq_begin(f.s, seq + 1);
+      load_window<T, W, V>(f, seq, t, t, d0, win);
+    }
+    if (t + kBwdBatch <= min(end, t1)) {
+      float xt[kBwdBatch][V], g[kBwdBatch][V];
+#pragma unroll
+      for (int i = 0; i < kBwdBatch; ++i) {
+        loadv<T, V>(x + (t + i) * f.x_pitch + d0, xt[i]);
+        loadv<T, V>(dy + (t + i) * p.dy_pitch + d0, g[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kBwdBatch; ++i) token(t + i, xt[i], g[i], true);
+      t += kBwdBatch;
+    } else {
+      float xt[V], g[V];
+      loadv<T, V>(x + t * f.x_pitch + d0, xt);
+      loadv<T, V>(dy + t * p.dy_pitch + d0, g);
+      token(t, xt, g, t < t1);
+      ++t;
+    }
+    if (t == end) {  // acc[k] is row end - (W-1) + k
 #pragma unroll
       for (int k = 0; k < W - 1; ++k) {
         if (p.dlast) {
@@ -185,7 +227,6 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvBwdParams p, int grou
         for (int v = 0; v < V; ++v) acc[k][v] = 0.f;
       }
     }
-    shift<W, V>(win, xt);
   }
 #pragma unroll
   for (int k = 0; k <= W; ++k)
@@ -239,31 +280,35 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvStepParams p, int gr
   storev<T, V>(y, o);
 }
 
-bool aligned16(std::initializer_list<const void*> ps) {
+bool aligned(std::initializer_list<const void*> ps, int dtype) {
   for (const void* q : ps)
-    if (reinterpret_cast<uintptr_t>(q) % 16) return false;
+    if (reinterpret_cast<uintptr_t>(q) % (dtype == GDN_DTYPE_BF16 ? 8 : 16)) return false;
   return true;
 }
 
-// f(T{}, W, V): the instance for these types and widths; vec: 16-byte vectors are possible.
+// f(T{}, W, V): the instance for these types and widths; vec: four channels at once are possible.
 template <typename F>
 hipError_t dispatch(int dtype, int W, bool vec, F&& f) {
+  using std::integral_constant;
   auto taps = [&](auto t, auto v) {
     switch (W) {
-      case 2: return f(t, std::integral_constant<int, 2>{}, v);
-      case 3: return f(t, std::integral_constant<int, 3>{}, v);
-      default: return f(t, std::integral_constant<int, 4>{}, v);
+      case 2: return f(t, integral_constant<int, 2>{}, v);
+      case 3: return f(t, integral_constant<int, 3>{}, v);
+      default: return f(t, integral_constant<int, 4>{}, v);
     }
   };
-  using One = std::integral_constant<int, 1>;
-  if (dtype == GDN_DTYPE_BF16)
-    return vec ? taps(bf16{}, std::integral_constant<int, 8>{}) : taps(bf16{}, One{});
-  return vec ? taps(float{}, std::integral_constant<int, 4>{}) : taps(float{}, One{});
+  auto width = [&](auto t) {
+    return vec ? taps(t, integral_constant<int, 4>{}) : taps(t, integral_constant<int, 1>{});
+  };
+  return dtype == GDN_DTYPE_BF16 ? width(bf16{}) : width(float{});
 }
 
-int vec_of(int dtype) { return dtype == GDN_DTYPE_BF16 ? 8 : 4; }
-
-constexpr int kBwdTile = 64;
+// Tokens of a forward tile: 32, or fewer where that would leave the chip without 8 waves a SIMD.
+int fwd_tile(int rows, int groups) {
+  int tile = 32;
+  while (tile > kFwdBatch && (int64_t)((rows + tile - 1) / tile) * groups < 8192 * 64) tile /= 2;
+  return tile;
+}
 
 }  // namespace
 
@@ -272,11 +317,10 @@ size_t conv_bwd_ws_bytes(int rows, int D, int W) {
 }
 
 hipError_t launch_conv_fwd(const ConvParams& p, int dtype, hipStream_t st) {
-  const int V = vec_of(dtype);
-  const bool vec = p.D % V == 0 && p.x_pitch % V == 0 && aligned16({p.x, p.init, p.y, p.last});
+  const bool vec = p.D % 4 == 0 && p.x_pitch % 4 == 0 && aligned({p.x, p.init, p.y, p.last}, dtype);
   return dispatch(dtype, p.W, vec, [&](auto t, auto w, auto v) {
     const int groups = p.D / v;
-    const int tile = 16;
+    const int tile = fwd_tile(p.s.rows, groups);
     const int64_t threads = (int64_t)((p.s.rows + tile - 1) / tile) * groups;
     conv_fwd_kernel<decltype(t), w(), v()><<<dim3((unsigned)((threads + 255) / 256)), 256, 0, st>>>(p, groups, tile);
     return hipGetLastError();
@@ -284,10 +328,9 @@ hipError_t launch_conv_fwd(const ConvParams& p, int dtype, hipStream_t st) {
 }
 
 hipError_t launch_conv_bwd(const ConvBwdParams& p, int dtype, hipStream_t st) {
-  const int V = vec_of(dtype);
   const ConvParams& f = p.f;
-  const bool vec = f.D % V == 0 && f.x_pitch % V == 0 && p.dy_pitch % V == 0 &&
-                   aligned16({f.x, f.init, p.dy, p.dlast, p.dx, p.dinit});
+  const bool vec = f.D % 4 == 0 && f.x_pitch % 4 == 0 && p.dy_pitch % 4 == 0 &&
+                   aligned({f.x, f.init, p.dy, p.dlast, p.dx, p.dinit}, dtype);
   return dispatch(dtype, f.W, vec, [&](auto t, auto w, auto v) {
     const int groups = f.D / v;
     const int tiles = (f.s.rows + kBwdTile - 1) / kBwdTile;
@@ -303,8 +346,7 @@ hipError_t launch_conv_bwd(const ConvBwdParams& p, int dtype, hipStream_t st) {
 }
 
 hipError_t launch_conv_step(const ConvStepParams& p, int dtype, hipStream_t st) {
-  const int V = vec_of(dtype);
-  const bool vec = p.D % V == 0 && p.x_pitch % V == 0 && aligned16({p.x, p.state, p.y});
+  const bool vec = p.D % 4 == 0 && p.x_pitch % 4 == 0 && aligned({p.x, p.state, p.y}, dtype);
   return dispatch(dtype, p.W, vec, [&](auto t, auto w, auto v) {
     const int groups = p.D / v;
     const int per_row = (groups + 255) / 256;

@@ -26,21 +26,20 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for_impl(static_cast<F&&>(f), std::make_integer_sequence<int, N>{});
 }
 
-// V consecutive values as fp32 and back.  V * sizeof(T) is 16 bytes (one access, 16-byte aligned)
-// or V is 1.
+// V consecutive values as fp32 and back: one access of 8 or 16 bytes, aligned to its size, or V is 1.
 template <typename T, int V>
 __device__ __forceinline__ void loadv(const T* p, float (&x)[V]) {
   if constexpr (V == 1) {
     x[0] = to_f(*p);
   } else {
-    static_assert(V * sizeof(T) == 16, "one 16-byte access");
-    const u32x4v r = *reinterpret_cast<const u32x4v*>(p);
-    if constexpr (sizeof(T) == 4) {
+    constexpr int WORDS = V * sizeof(T) / 4;
+    typedef unsigned Words __attribute__((ext_vector_type(WORDS)));
+    const Words r = *reinterpret_cast<const Words*>(p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < WORDS; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        x[i] = __uint_as_float(r[i]);
+      } else {
         x[2 * i] = __uint_as_float(r[i] << 16);
         x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
       }
@@ -53,7 +52,6 @@ __device__ __forceinline__ void storev(T* p, const float (&x)[V]) {
   if constexpr (V == 1) {
     *p = to_t<T>(x[0]);
   } else {
-    static_assert(V * sizeof(T) == 16, "one 16-byte access");
     typedef T Vt __attribute__((ext_vector_type(V)));
     Vt r;
 #pragma unroll
