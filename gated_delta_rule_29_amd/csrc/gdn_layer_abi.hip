@@ -123,6 +123,7 @@ int check_scan(const Scan& a, int D, int N, int dtype) {
   GDN_TRY(check_pitch("dt", a.dt, a.dt_pitch, D));
   GDN_TRY(check_pitch("z", a.z, a.z_pitch, D));
   GDN_TRY(check_pitch("Bm", a.Bm, a.b_pitch, N));
+  GDN_TRY(check_state("A", a.A, N));
   return check_pitch("Cm", a.Cm, a.c_pitch, N);
 }
 

@@ -181,47 +181,61 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmParams p, int per_seq)
 }
 
 // One token a row.  A row whose slot is outside the cache, or is an earlier row's, changes nothing
-// and gives 0.
-template <typename T, int LN, int NPL>
+// and gives 0.  A workgroup has U * 256 / LN channels of one row; bound by the states' bytes, so
+// everything that a lane reads is asked for before anything is waited for.
+template <typename T, int LN, int NPL, int U>
 __global__ __launch_bounds__(256) void ssm_step_kernel(SsmStepParams p, int groups) {
-  constexpr int CH = 64 / LN;
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, j = lane % LN;
-  const int b = blockIdx.x / groups;
-  const int c = ((blockIdx.x - b * groups) * 4 + wv) * CH + lane / LN;
-  const bool cv = c < p.D;
+  constexpr int CH = 256 / LN;
+  const int b = blockIdx.x / groups, grp = blockIdx.x - b * groups, j = threadIdx.x % LN;
   const int slot = p.slots ? p.slots[b] : b;
   bool live = slot >= 0 && slot < p.S;
-  float h[NPL];
+  const int other = p.slots && (int)threadIdx.x < b ? p.slots[threadIdx.x] : -1;
   float* st = p.state + (live ? (int64_t)slot * p.D * p.N : 0);
-  if (live && cv) load_state<NPL>(st, c, j, p.N, h);
-  if (p.slots && live) live = !slot_taken(p.slots, b, slot);  // slot is the workgroup's
-  if (!cv) return;
-  float y = 0.f;
-  if (live) {
-    const float x = to_f(static_cast<const T*>(p.x)[b * p.x_pitch + c]);
-    float de = to_f(static_cast<const T*>(p.dt)[b * p.dt_pitch + c]) + (p.dt_bias ? p.dt_bias[c] : 0.f);
-    if (p.softplus) de = softplus_f(de, nullptr);
-    const float dx = de * x;
+  float h[U][NPL], A2[U][NPL], bn[NPL], cn[NPL], x[U], dt[U], z[U], bias[U], skip[U];
+  int c[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    c[u] = (grp * U + u) * CH + threadIdx.x / LN;
+    const int cc = min(c[u], p.D - 1);
+    load_state<NPL>(st, cc, j, p.N, h[u]);
+    load_state<NPL>(p.A, cc, j, p.N, A2[u]);
+    x[u] = to_f(static_cast<const T*>(p.x)[b * p.x_pitch + cc]);
+    dt[u] = to_f(static_cast<const T*>(p.dt)[b * p.dt_pitch + cc]);
+    z[u] = to_f(p.z ? static_cast<const T*>(p.z)[b * p.z_pitch + cc] : static_cast<const T*>(p.x)[b * p.x_pitch + cc]);
+    bias[u] = p.dt_bias ? p.dt_bias[cc] : 0.f;
+    skip[u] = p.skip ? p.skip[cc] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int n = j * NPL + i, nn = min(n, p.N - 1);
+    const float bv = to_f(static_cast<const T*>(p.Bm)[b * p.b_pitch + nn]), cv = to_f(static_cast<const T*>(p.Cm)[b * p.c_pitch + nn]);
+    bn[i] = n < p.N ? bv : 0.f;
+    cn[i] = n < p.N ? cv : 0.f;
+  }
+  if (p.slots && live) {  // slot is the workgroup's
+    int taken = other == slot;
+    for (int i = threadIdx.x + 256; i < b; i += 256) taken |= p.slots[i] == slot;
+    live = !__syncthreads_or(taken);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float de = dt[u] + bias[u];
+    const float sp = softplus_f(de, nullptr);
+    de = p.softplus ? sp : de;
+    const float dx = de * x[u];
     float acc = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      const int n = j * NPL + i;
-      if (n < p.N) {
-        const float bn = to_f(static_cast<const T*>(p.Bm)[b * p.b_pitch + n]);
-        const float cn = to_f(static_cast<const T*>(p.Cm)[b * p.c_pitch + n]);
-        const float a = __builtin_amdgcn_exp2f(de * (p.A[(int64_t)c * p.N + n] * kLog2e));
-        h[i] = __builtin_fmaf(a, h[i], dx * bn);
-        acc = __builtin_fmaf(cn, h[i], acc);
-      }
+      h[u][i] = __builtin_fmaf(__builtin_amdgcn_exp2f(de * (A2[u][i] * kLog2e)), h[u][i], dx * bn[i]);
+      acc = __builtin_fmaf(cn[i], h[u][i], acc);
     }
-    store_state<NPL>(st, c, j, p.N, h);
-    y = group_sum<LN>(acc) + (p.skip ? p.skip[c] * x : 0.f);
-    if (p.z) {
-      const float z = to_f(static_cast<const T*>(p.z)[b * p.z_pitch + c]);
-      y *= z * sigmoid_f(z);
+    const float s = z[u] * sigmoid_f(z[u]);
+    const float y = (group_sum<LN>(acc) + skip[u] * x[u]) * (p.z ? s : 1.f);
+    if (c[u] < p.D) {
+      if (live) store_state<NPL>(st, c[u], j, p.N, h[u]);
+      if (j == 0) static_cast<T*>(p.y)[(int64_t)b * p.D + c[u]] = to_t<T>(live ? y : 0.f);
     }
   }
-  if (j == 0) static_cast<T*>(p.y)[(int64_t)b * p.D + c] = to_t<T>(y);
 }
 
 }  // namespace
@@ -264,9 +278,15 @@ hipError_t launch_ssm_fwd(SsmParams p, int dtype, void* ws, hipStream_t st) {
 
 hipError_t launch_ssm_step(const SsmStepParams& p, int dtype, hipStream_t st) {
   return ssm_dispatch(dtype, p.N, [&](auto t, auto ln, auto npl) {
-    constexpr int LN = decltype(ln)::value, NPL = decltype(npl)::value;
-    const int groups = (p.D + 4 * (64 / LN) - 1) / (4 * (64 / LN));
-    ssm_step_kernel<decltype(t), LN, NPL><<<dim3((unsigned)(groups * p.B)), 256, 0, st>>>(p, groups);
+    using T = decltype(t);
+    constexpr int LN = decltype(ln)::value, NPL = decltype(npl)::value, CH = 256 / LN;
+    // Four sets of channels a workgroup where that still gives each CU eight; one where the call is
+    // small and spreading it shortens it.
+    const int64_t one = (int64_t)p.B * ((p.D + CH - 1) / CH);
+    const int u = one >= 4 * 8 * 256 ? 4 : 1, groups = (p.D + CH * u - 1) / (CH * u);
+    const dim3 grid((unsigned)(groups * p.B));
+    if (u == 4) ssm_step_kernel<T, LN, NPL, 4><<<grid, 256, 0, st>>>(p, groups);
+    else ssm_step_kernel<T, LN, NPL, 1><<<grid, 256, 0, st>>>(p, groups);
     return hipGetLastError();
   });
 }

@@ -639,7 +639,7 @@ GDN_API int gdn_bwd_dhu_varlen(const void* q, const void* k, const void* w, cons
  *  - dtype is that of the activations (inputs and outputs that are not said to be fp32);
  *    all arithmetic, states and sums over tokens or channels are fp32, each result rounded once.
  *  - Pointers have their type's alignment; 16-byte alignment (and pitches and widths that are
- *    multiples of 16 bytes) is faster.  fp32 state tensors [.., D, N] must be 16-byte
+ *    multiples of 16 bytes) is faster.  fp32 [.., D, N] tensors (A, states) must be 16-byte
  *    aligned where N is a multiple of 4.
  *  - Sums over rows and channels are joined in a fixed order: results are deterministic.
  * ------------------------------------------------------------------------------------------ */

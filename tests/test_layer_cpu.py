@@ -88,7 +88,7 @@ def test_scan_codes():
     L, lib = _lib()
     for bad in (dict(x=None), dict(dt=None), dict(A=None), dict(B_=None), dict(C_=None), dict(y=None), dict(B=0),
                 dict(T=0), dict(D=0), dict(N=0), dict(ty=3), dict(xp=7), dict(bp=15), dict(z=FAKE, zp=7),
-                dict(h0=ODD), dict(ht=ODD), dict(h=ODD), dict(B=1 << 16, T=1 << 16)):
+                dict(A=ODD), dict(h0=ODD), dict(ht=ODD), dict(h=ODD), dict(B=1 << 16, T=1 << 16)):
         assert _scan(lib, **bad) == L.ERR_INVALID, bad
     assert _scan(lib, N=65, bp=65) == L.ERR_UNSUPPORTED
     # a long sequence of few channels is cut and needs a workspace; a short or a wide one does not
