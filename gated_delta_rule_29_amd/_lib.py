@@ -88,6 +88,7 @@ SIGNATURES = {
     "ssm_scan_bwd_varlen_workspace_bytes": (SZ, [P, I, I, I]),
     "ssm_scan_bwd_varlen": (I, [P, L, P, P, L, P, L, P, P, L, P, L, P, P, I, P, P, L, P, P] + [P] * 9
                             + [I, I, I, I, I, P, SZ, P]),
+    "ssm_scan_num_chunks": (I, [P, I]),
     "ssm_step": (I, [P, L, P, L, P, P, L, P, L, P, P, L, P, P, P, P, I, I, I, I, I, I, P]),
     "rms_norm_fwd": (I, [P, L, P, L, P, F, P, P, P, I, I, I, I, P]),
     "rms_norm_q8_fwd": (I, [P, L, P, L, P, F, I, P, P, P, I, I, I, I, P]),

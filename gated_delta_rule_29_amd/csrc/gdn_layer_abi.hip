@@ -301,6 +301,14 @@ int causal_conv_step(const void* x, int64_t x_pitch, const float* w, const float
   return e == hipSuccess ? ok() : hip_fail(e, "causal_conv_step launch");
 }
 
+int ssm_scan_num_chunks(const int* cu_seqlens_host, int N_seq) {
+  if (!sizable(cu_seqlens_host, N_seq, 1, 1)) return -1;
+  int64_t total = 0;
+  for (int i = 0; i < N_seq; ++i)
+    total += ((int64_t)cu_seqlens_host[i + 1] - cu_seqlens_host[i] + GDN_SSM_CHUNK - 1) / GDN_SSM_CHUNK;
+  return total > INT32_MAX ? -1 : (int)total;
+}
+
 size_t ssm_scan_fwd_workspace_bytes(int B, int T, int D, int N) {
   if (B <= 0 || T <= 0 || D <= 0 || N <= 0 || N > gdn::kSsmMaxN || (int64_t)B * T > INT32_MAX) return 0;
   return fwd_ws(dense_split(false, B, T, D, N), B, D, N);

@@ -724,7 +724,9 @@ GDN_API int ssm_scan_fwd(const void* x, int64_t x_pitch, const void* dt, int64_t
                          int B, int T, int D, int N, int softplus, int dtype, void* workspace,
                          size_t workspace_bytes, void* stream);
 /* The packed form: tokens [1, T_total, .], h0 and ht [N_seq, D, N]; h [1, NC_total, D, N] with the
- * sequences' chunks in order, NC_total = sum_i ceil(length_i / GDN_SSM_CHUNK). */
+ * sequences' chunks in order, NC_total = ssm_scan_num_chunks: sum_i ceil(length_i / GDN_SSM_CHUNK), or -1
+ * where the HOST offsets are malformed (host-only, as gdn_varlen_num_chunks). */
+GDN_API int ssm_scan_num_chunks(const int* cu_seqlens_host, int N_seq);
 GDN_API size_t ssm_scan_fwd_varlen_workspace_bytes(const int* cu_seqlens_host, int N_seq, int D,
                                                    int N);
 GDN_API int ssm_scan_fwd_varlen(const void* x, int64_t x_pitch, const void* dt, int64_t dt_pitch,

@@ -99,7 +99,10 @@ def test_scan_codes():
     assert lib.ssm_scan_fwd_workspace_bytes(1, 64, 8, 65) == 0
     keep, p = _cu(0, 64, 4160)
     assert lib.ssm_scan_fwd_varlen_workspace_bytes(p, 2, 8, 16) > 0
+    keep, p = _cu(0, 1, 17, 50)
+    assert lib.ssm_scan_num_chunks(p, 3) == 1 + 1 + 3
     keep, p = _cu(0, 64, 64)
+    assert lib.ssm_scan_num_chunks(p, 2) == -1
     assert lib.ssm_scan_fwd_varlen_workspace_bytes(p, 2, 8, 16) == 0
     assert lib.ssm_scan_bwd_varlen_workspace_bytes(p, 2, 8, 16) == 0
     assert lib.ssm_scan_bwd_varlen_workspace_bytes(None, 2, 8, 16) == 0
