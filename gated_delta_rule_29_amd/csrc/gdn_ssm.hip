@@ -9,7 +9,7 @@
 // holds 64 / LN channels.  Lane j of a channel also owns every LN-th token: it loads that token's x,
 // dt and z and forms its step size, gate and output once, and the channel's other lanes read the
 // two values they need through lane-exchange operands.  B and C, shared by all channels, are staged as
-// fp32 in LDS, a block at a time.  Everything is fp32 but the inputs' and outputs' own types.
+// fp32 in LDS.  Everything is fp32 but the inputs' and outputs' own types.
 //
 // Long sequences are cut into segments where there are too few channels to fill the chip: a first
 // kernel forms each segment's end state from a zero start, a second joins them (a segment's whole
@@ -21,8 +21,8 @@ namespace gdn {
 
 namespace {
 
-// The state from a zero start and the summed step sizes of a segment.  No prefetch: eight waves a SIMD
-// hide the loads.
+// The state from a zero start and the summed step sizes of a segment, 32 tokens at a time (97 us at the
+// size below, 101 with 16): the recurrence without its outputs.
 template <typename T, int LN, int NPL>
 __global__ __launch_bounds__(256) void ssm_fwd_summary_kernel(SsmParams p, int groups) {
   constexpr int NP = LN * NPL, TL = kSsmBlock / LN;
@@ -55,13 +55,13 @@ __global__ __launch_bounds__(256) void ssm_fwd_summary_kernel(SsmParams p, int g
       const float dx = de * of_bits<T>(xr[g]);
       dsum += de;
       static_for<LN>([&](auto k) {
-        const float dk = lane_of<LN, k()>(de), xk = lane_of<LN, k()>(dx);
+        const float dk = shared_lane<LN, k()>(de), xk = shared_lane<LN, k()>(dx);
         float b[NPL], cf[NPL];
         read_bc<NPL>(bc + ((g * LN + k()) * NP + j * NPL) * 2, b, cf);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dk * A2[i]), h[i], xk * b[i]);
       });
-      __builtin_amdgcn_sched_barrier(0);  // keeps the exponentials of later tokens from filling the registers
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   if (w.cv) store_state<NPL>(p.seg_state + (int64_t)w.seg * p.D * p.N, w.c, j, p.N, h);
@@ -69,38 +69,23 @@ __global__ __launch_bounds__(256) void ssm_fwd_summary_kernel(SsmParams p, int g
   if (w.cv && j == 0) p.seg_sum[(int64_t)w.seg * p.D + w.c] = dsum;
 }
 
-// A block's inputs are asked for while the block before it is computed, its B and C go to the other of two
-// LDS buffers, and outputs are stored at the block's end, so that the 32 tokens are one stretch of
-// code without branches.
+// The scan proper, a chunk of 16 tokens at a time.  Bound by vector instructions: 20 of the 33 a token
+// and wave are the recurrence's own (16 channels x 4 states a lane: 2 products, an exponential and 2
+// fused multiply-adds each).  Seven waves a SIMD hide the loads; asking for a 32-token block's inputs a
+// block ahead took 99 registers and 177 us instead of 68 and 151 (4 x 2048 tokens x 4096 channels x
+// 16 states, bf16, states saved).
 template <typename T, int LN, int NPL>
 __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
-  constexpr int NP = LN * NPL, TL = kSsmBlock / LN;
-  __shared__ __align__(16) float bc[2][kSsmBlock * NP * 2];
+  constexpr int NP = LN * NPL, TL = kSsmChunk / LN;
+  __shared__ __align__(16) float bc[kSsmChunk * NP * 2];
   const Place<LN> w(p, groups);
   if (w.pc.seq < 0) return;
   const int j = w.j, cc = w.cc, t1 = w.t1;
-
   const bool gate = p.z;
   const void* zp = gate ? p.z : p.x;
   const int64_t zpitch = gate ? p.z_pitch : p.x_pitch;
   const unsigned vx = (unsigned)(j * (int)p.x_pitch + cc) * sizeof(T), vd = (unsigned)(j * (int)p.dt_pitch + cc) * sizeof(T),
                  vz = (unsigned)(j * (int)zpitch + cc) * sizeof(T);
-  unsigned xr[TL], dr[TL], zr[TL];
-  StageBC<T, NP, kSsmBlock, 256> st;
-  auto ask = [&](int tb) {
-    const int rows = min(t1 - tb, kSsmBlock);
-    const auto rx = window<T>(p.x, p.x_pitch, tb, rows, p.D), rd = window<T>(p.dt, p.dt_pitch, tb, rows, p.D),
-               rz = window<T>(zp, zpitch, tb, rows, p.D);
-#pragma unroll
-    for (int g = 0; g < TL; ++g) {
-      xr[g] = load_bits<T>(rx, vx + g * LN * (unsigned)p.x_pitch * sizeof(T));
-      dr[g] = load_bits<T>(rd, vd + g * LN * (unsigned)p.dt_pitch * sizeof(T));
-      zr[g] = load_bits<T>(rz, vz + g * LN * (unsigned)zpitch * sizeof(T));
-    }
-    st.load(p, tb, rows);
-  };
-  ask(w.t0);
-
   const int64_t DN = (int64_t)p.D * p.N;
   float A2[NPL], h[NPL];
   load_decay<NPL>(p, cc, j, A2);
@@ -109,36 +94,40 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
   float* save = nullptr;
   if (p.h) save = p.h + (find_piece_before(p.s, w.pc, kSsmChunk, w.lane) + (w.t0 - w.pc.begin) / kSsmChunk) * DN;
   const unsigned vy = w.cv ? (unsigned)(j * p.D + w.c) * sizeof(T) : kNowhere;
-  st.store(bc[0]);
-  __syncthreads();
 
-  int buf = 0;
-  for (int tb = w.t0; tb < t1; tb += kSsmBlock, buf ^= 1) {
-    float x[TL], z[TL], de[TL];
+  for (int tb = w.t0; tb < t1; tb += kSsmChunk) {
+    const int rows = min(t1 - tb, kSsmChunk);
+    const auto rx = window<T>(p.x, p.x_pitch, tb, rows, p.D), rd = window<T>(p.dt, p.dt_pitch, tb, rows, p.D),
+               rz = window<T>(zp, zpitch, tb, rows, p.D), ry = window<T>(p.y, p.D, tb, rows, p.D);
+    unsigned xr[TL], dr[TL], zr[TL];
 #pragma unroll
     for (int g = 0; g < TL; ++g) {
-      x[g] = of_bits<T>(xr[g]);
-      z[g] = of_bits<T>(zr[g]);
-      de[g] = of_bits<T>(dr[g]) + bias;
+      xr[g] = load_bits<T>(rx, vx + g * LN * (unsigned)p.x_pitch * sizeof(T));
+      dr[g] = load_bits<T>(rd, vd + g * LN * (unsigned)p.dt_pitch * sizeof(T));
+      zr[g] = load_bits<T>(rz, vz + g * LN * (unsigned)zpitch * sizeof(T));
     }
-    const bool more = tb + kSsmBlock < t1;
-    if (more) ask(tb + kSsmBlock);
-    const auto ry = window<T>(p.y, p.D, tb, min(t1 - tb, kSsmBlock), p.D);
+    StageBC<T, NP, kSsmChunk, 256> st;
+    st.load(p, tb, rows);
+    __syncthreads();
+    st.store(bc);
+    __syncthreads();
+    if (save) {
+      if (w.cv) store_state<NPL>(save, w.c, j, p.N, h);
+      save += DN;
+    }
 #pragma unroll
     for (int g = 0; g < TL; ++g) {
-      if (save && g * LN % kSsmChunk == 0 && tb + g * LN < t1) {
-        if (w.cv) store_state<NPL>(save, w.c, j, p.N, h);
-        save += DN;
-      }
-      const float sp = softplus_f(de[g], nullptr);
-      de[g] = p.softplus ? sp : de[g];
-      if (tb + g * LN + j >= t1) de[g] = 0.f;  // a token behind the end keeps the state as it is
-      const float dx = de[g] * x[g];
+      const float x = of_bits<T>(xr[g]), z = of_bits<T>(zr[g]);
+      float de = of_bits<T>(dr[g]) + bias;
+      const float sp = softplus_f(de, nullptr);
+      de = p.softplus ? sp : de;
+      if (g * LN + j >= rows) de = 0.f;  // a token behind the end keeps the state as it is
+      const float dx = de * x;
       float yp[LN];
       static_for<LN>([&](auto k) {
-        const float dk = lane_of<LN, k()>(de[g]), xk = lane_of<LN, k()>(dx);
+        const float dk = shared_lane<LN, k()>(de), xk = shared_lane<LN, k()>(dx);
         float b[NPL], cf[NPL];
-        read_bc<NPL>(bc[buf] + ((g * LN + k()) * NP + j * NPL) * 2, b, cf);
+        read_bc<NPL>(bc + ((g * LN + k()) * NP + j * NPL) * 2, b, cf);
         float acc = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
@@ -147,14 +136,11 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
         }
         yp[k()] = acc;
       });
-      float y = reduce_scatter<LN>(yp, j) + skip * x[g];
-      const float s = z[g] * sigmoid_f(z[g]);
+      float y = reduce_scatter<LN>(yp, j) + skip * x;
+      const float s = z * sigmoid_f(z);
       y *= gate ? s : 1.f;
       store_bits<T>(ry, to_t<T>(y), vy + g * LN * (unsigned)p.D * sizeof(T));  // dropped behind the end
-    }
-    if (more) {
-      st.store(bc[buf ^ 1]);  // read last before the barrier of the block before
-      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);  // keeps the exponentials of later tokens from filling the registers
     }
   }
   if (p.ht && t1 == w.pc.end && w.cv) store_state<NPL>(p.ht + w.pc.seq * DN, w.c, j, p.N, h);
@@ -240,6 +226,11 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmStepParams p, int grou
 
 }  // namespace
 
+// Long sequences are cut where the channels give fewer than two waves a SIMD (2048): the summary costs
+// 0.6 of the scan proper, less than what too few waves cost.  Segments are then as short as gives
+// eight waves a SIMD.  4 sequences of 2048 tokens x 4096 channels x 16 states (scan + summary, us; with an
+// earlier form of the scan): uncut, one wave, 276; cut for two 212 + 122, for four 187 + 108, for
+// eight 179 + 102.  Two waves uncut: 212 by the same row.
 int ssm_segment(bool backward, int rows, int nseq, int max_len, int D, int N) {
   const int ch = N <= 16 ? 16 : 4;  // channels of a wave
   const int64_t per_seg = (D + ch - 1) / ch;

@@ -147,7 +147,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_summary_kernel(SsmBwdParams p, in
       dsum += tk.de;
       static_for<LN>([&](auto r) {
         constexpr int k = LN - 1 - r();
-        const float dk = lane_of<LN, k>(tk.de), gk = lane_of<LN, k>(tk.gy);
+        const float dk = shared_lane<LN, k>(tk.de), gk = shared_lane<LN, k>(tk.gy);
         float b[NPL], cf[NPL];
         read_bc<NPL>(bc + ((q * LN + k) * NP + j * NPL) * 2, b, cf);
 #pragma unroll
