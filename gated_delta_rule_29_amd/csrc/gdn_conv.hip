@@ -339,9 +339,7 @@ hipError_t launch_conv_bwd(const ConvBwdParams& p, int dtype, hipStream_t st) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t cols = (int64_t)(f.W + 1) * f.D;
-    column_sum_kernel<<<dim3((unsigned)((cols + 63) / 64)), 1024, 0, st>>>(
-        p.part, tiles, cols, ConvWeightOut{p.dw, p.dbias, f.D, f.W});
-    return hipGetLastError();
+    return column_sum(p.part, tiles, cols, ConvWeightOut{p.dw, p.dbias, f.D, f.W}, st);
   });
 }
 

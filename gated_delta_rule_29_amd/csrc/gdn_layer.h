@@ -75,6 +75,12 @@ constexpr int kSsmChunk = 16;
 constexpr int kSsmBlock = 32;
 constexpr int kSsmMaxN = 64;
 
+// How long sequences are cut: segments of `seg` tokens (a multiple of kSsmBlock), nseg in all, are
+// summarised and joined; the pass proper takes `main` tokens (a multiple of seg) at a time, nmain in all.
+struct SsmSplit {
+  int seg, nseg, main, nmain;
+};
+
 struct SsmParams {
   const void* x;        // rows of D
   const void* dt;
@@ -92,8 +98,7 @@ struct SsmParams {
   Seqs s;
   int D, N;
   bool softplus;
-  // the split of long sequences: segments of `seg` tokens (a multiple of kSsmBlock), nseg in all
-  int seg, nseg;
+  SsmSplit split;
   float* seg_state;     // workspace [nseg, D, N]: a segment's end from a zero start, then its start
   float* seg_sum;       // workspace [nseg, D]: the segment's summed step sizes
 };
@@ -110,7 +115,7 @@ struct SsmBwdParams {
   float *ddt_bias;      // [D] or nullptr
   float *dh0;           // [n, D, N] or nullptr
   float* part_bc;       // workspace [channel groups][rows][2][N]
-  float* part_a;        // workspace [nseg][D][N + 2]
+  float* part_a;        // workspace [nmain][D][N + 2]
 };
 
 struct SsmStepParams {
@@ -124,11 +129,10 @@ struct SsmStepParams {
   bool softplus;
 };
 
-// The split that a forward (or backward) call of these sizes uses: tokens a segment.  max_len:
-// the longest sequence.
-int ssm_segment(bool backward, int rows, int nseq, int max_len, int D, int N);
-size_t ssm_fwd_ws_bytes(int nseg, int D, int N);
-size_t ssm_bwd_ws_bytes(int nseg, int rows, int D, int N);
+// The split of a call over n sequences: from their offsets on the host, or (cu null) of T tokens each.
+SsmSplit ssm_split(bool backward, const int* cu, int n, int T, int D, int N);
+size_t ssm_fwd_ws_bytes(const SsmSplit& sp, int n, int D, int N);
+size_t ssm_bwd_ws_bytes(const SsmSplit& sp, int rows, int D, int N);
 hipError_t launch_ssm_fwd(SsmParams p, int dtype, void* ws, hipStream_t st);
 hipError_t launch_ssm_bwd(SsmBwdParams p, int dtype, void* ws, hipStream_t st);
 hipError_t launch_ssm_step(const SsmStepParams& p, int dtype, hipStream_t st);

@@ -127,25 +127,10 @@ int check_scan(const Scan& a, int D, int N, int dtype) {
   return check_pitch("Cm", a.Cm, a.c_pitch, N);
 }
 
-// Tokens of a segment and segments in all.
-struct Split {
-  int seg, nseg;
-};
-Split dense_split(bool bwd, int B, int T, int D, int N) {
-  Split r;
-  r.seg = gdn::ssm_segment(bwd, B * T, B, T, D, N);
-  r.nseg = B * ((T + r.seg - 1) / r.seg);
-  return r;
-}
-Split packed_split(bool bwd, const int* cu, int n, int D, int N) {
-  int longest = 1;
-  for (int i = 0; i < n; ++i) longest = cu[i + 1] - cu[i] > longest ? cu[i + 1] - cu[i] : longest;
-  Split r;
-  r.seg = gdn::ssm_segment(bwd, cu[n], n, longest, D, N);
-  r.nseg = 0;
-  for (int i = 0; i < n; ++i) r.nseg += (cu[i + 1] - cu[i] + r.seg - 1) / r.seg;
-  return r;
-}
+using Split = gdn::SsmSplit;
+
+Split dense_split(bool bwd, int B, int T, int D, int N) { return gdn::ssm_split(bwd, nullptr, B, T, D, N); }
+Split packed_split(bool bwd, const int* cu, int n, int D, int N) { return gdn::ssm_split(bwd, cu, n, 0, D, N); }
 
 // Whether the offsets can be sized at all (the calls check them in full).
 bool sizable(const int* cu, int n, int D, int N) {
@@ -155,15 +140,13 @@ bool sizable(const int* cu, int n, int D, int N) {
   return true;
 }
 
-size_t fwd_ws(const Split& sp, int n, int D, int N) { return sp.nseg > n ? gdn::ssm_fwd_ws_bytes(sp.nseg, D, N) : 0; }
-
 gdn::SsmParams scan_params(const gdn::Seqs& s, const Split& sp, const Scan& a, int D, int N, int softplus) {
   gdn::SsmParams p{};
   p.x = a.x; p.dt = a.dt; p.z = a.z; p.Bm = a.Bm; p.Cm = a.Cm;
   p.x_pitch = a.x_pitch; p.dt_pitch = a.dt_pitch; p.z_pitch = a.z_pitch;
   p.b_pitch = a.b_pitch; p.c_pitch = a.c_pitch;
   p.A = a.A; p.skip = a.skip; p.dt_bias = a.dt_bias;
-  p.s = s; p.D = D; p.N = N; p.softplus = softplus != 0; p.seg = sp.seg; p.nseg = sp.nseg;
+  p.s = s; p.D = D; p.N = N; p.softplus = softplus != 0; p.split = sp;
   return p;
 }
 
@@ -180,7 +163,7 @@ int scan_fwd(const gdn::Seqs& s, const Split& sp, const Scan& a, const float* h0
   GDN_TRY(check_state("ht", ht, N));
   GDN_TRY(check_state("h", h, N));
   GDN_TRY(check_scan_grid(s, sp, D, N));
-  GDN_TRY(check_workspace(ws, ws_bytes, fwd_ws(sp, s.n, D, N)));
+  GDN_TRY(check_workspace(ws, ws_bytes, gdn::ssm_fwd_ws_bytes(sp, s.n, D, N)));
   gdn::SsmParams p = scan_params(s, sp, a, D, N, softplus);
   p.h0 = h0; p.y = y; p.ht = ht; p.h = h;
   const hipError_t e = gdn::launch_ssm_fwd(p, dtype, ws, static_cast<hipStream_t>(stream));
@@ -205,7 +188,7 @@ int scan_bwd(const gdn::Seqs& s, const Split& sp, const Scan& a, const void* dy,
   GDN_TRY(check_state("dh0", o.dh0, N));
   GDN_TRY(check_scan_grid(s, sp, D, N));
   GDN_TRY(check_grid(s.rows, (2 * N + 63) / 64, "ssm_scan_bwd"));
-  GDN_TRY(check_workspace(ws, ws_bytes, gdn::ssm_bwd_ws_bytes(sp.nseg, s.rows, D, N)));
+  GDN_TRY(check_workspace(ws, ws_bytes, gdn::ssm_bwd_ws_bytes(sp, s.rows, D, N)));
   gdn::SsmBwdParams p{};
   p.f = scan_params(s, sp, a, D, N, softplus);
   p.f.h = const_cast<float*>(h);
@@ -311,22 +294,22 @@ int ssm_scan_num_chunks(const int* cu_seqlens_host, int N_seq) {
 
 size_t ssm_scan_fwd_workspace_bytes(int B, int T, int D, int N) {
   if (B <= 0 || T <= 0 || D <= 0 || N <= 0 || N > gdn::kSsmMaxN || (int64_t)B * T > INT32_MAX) return 0;
-  return fwd_ws(dense_split(false, B, T, D, N), B, D, N);
+  return gdn::ssm_fwd_ws_bytes(dense_split(false, B, T, D, N), B, D, N);
 }
 
 size_t ssm_scan_fwd_varlen_workspace_bytes(const int* cu_seqlens_host, int N_seq, int D, int N) {
   if (!sizable(cu_seqlens_host, N_seq, D, N)) return 0;
-  return fwd_ws(packed_split(false, cu_seqlens_host, N_seq, D, N), N_seq, D, N);
+  return gdn::ssm_fwd_ws_bytes(packed_split(false, cu_seqlens_host, N_seq, D, N), N_seq, D, N);
 }
 
 size_t ssm_scan_bwd_workspace_bytes(int B, int T, int D, int N) {
   if (B <= 0 || T <= 0 || D <= 0 || N <= 0 || N > gdn::kSsmMaxN || (int64_t)B * T > INT32_MAX) return 0;
-  return gdn::ssm_bwd_ws_bytes(dense_split(true, B, T, D, N).nseg, B * T, D, N);
+  return gdn::ssm_bwd_ws_bytes(dense_split(true, B, T, D, N), B * T, D, N);
 }
 
 size_t ssm_scan_bwd_varlen_workspace_bytes(const int* cu_seqlens_host, int N_seq, int D, int N) {
   if (!sizable(cu_seqlens_host, N_seq, D, N)) return 0;
-  return gdn::ssm_bwd_ws_bytes(packed_split(true, cu_seqlens_host, N_seq, D, N).nseg, cu_seqlens_host[N_seq], D, N);
+  return gdn::ssm_bwd_ws_bytes(packed_split(true, cu_seqlens_host, N_seq, D, N), cu_seqlens_host[N_seq], D, N);
 }
 
 int ssm_scan_fwd(const void* x, int64_t x_pitch, const void* dt, int64_t dt_pitch, const float* A, const void* Bm,

@@ -175,6 +175,11 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
     out(c, t);
   }
 }
+template <typename Out>
+hipError_t column_sum(const float* part, int rows, int64_t cols, Out out, hipStream_t st) {
+  column_sum_kernel<<<dim3((unsigned)((cols + 63) / 64)), 1024, 0, st>>>(part, rows, cols, out);
+  return hipGetLastError();
+}
 
 // Whether a row before row b uses the same slot: the first row of a slot is the one that counts.
 // Called by all threads of the workgroup.

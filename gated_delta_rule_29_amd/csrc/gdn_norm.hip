@@ -362,8 +362,7 @@ hipError_t launch_norm_bwd(const NormBwdParams& p, int dtype, int sdtype, hipStr
       norm_bwd_kernel<decltype(t), decltype(rt), v(), TPR, nv()><<<dim3((groups + rpw - 1) / rpw), wg, 0, st>>>(p, groups);
       hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
-      column_sum_kernel<<<dim3((unsigned)((p.D + 63) / 64)), 1024, 0, st>>>(p.part, groups, (int64_t)p.D, NormWeightOut{p.dw});
-      return hipGetLastError();
+      return column_sum(p.part, groups, p.D, NormWeightOut{p.dw}, st);
     });
   });
 }

@@ -27,7 +27,7 @@ template <typename T, int LN, int NPL>
 __global__ __launch_bounds__(256) void ssm_fwd_summary_kernel(SsmParams p, int groups) {
   constexpr int NP = LN * NPL, TL = kSsmBlock / LN;
   __shared__ __align__(16) float bc[kSsmBlock * NP * 2];
-  const Place<LN> w(p, groups);
+  const Place<LN> w(p, groups, p.split.seg);
   if (w.pc.seq < 0 || w.t1 == w.pc.end) return;  // nothing follows the last segment
   const int j = w.j, cc = w.cc;
   float A2[NPL], h[NPL] = {};
@@ -78,7 +78,7 @@ template <typename T, int LN, int NPL>
 __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
   constexpr int NP = LN * NPL, TL = kSsmChunk / LN;
   __shared__ __align__(16) float bc[kSsmChunk * NP * 2];
-  const Place<LN> w(p, groups);
+  const Place<LN> w(p, groups, p.split.seg);
   if (w.pc.seq < 0) return;
   const int j = w.j, cc = w.cc, t1 = w.t1;
   const bool gate = p.z;
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmParams p, int per_seq)
   const int64_t e = (int64_t)(blockIdx.x - seq * per_seq) * 256 + threadIdx.x;
   const int lane = threadIdx.x & 63;
   const int64_t DN = (int64_t)p.D * p.N;
-  const SeqPieces sp = pieces_of(p.s, seq, p.seg, lane);
+  const SeqPieces sp = pieces_of(p.s, seq, p.split.seg, lane);
   if (e >= DN) return;
   const int64_t d = e / p.N;
   const float a = p.A[e] * kLog2e;
@@ -231,29 +231,50 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmStepParams p, int grou
 // eight waves a SIMD.  4 sequences of 2048 tokens x 4096 channels x 16 states (scan + summary, us; with an
 // earlier form of the scan): uncut, one wave, 276; cut for two 212 + 122, for four 187 + 108, for
 // eight 179 + 102.  Two waves uncut: 212 by the same row.
-int ssm_segment(bool backward, int rows, int nseq, int max_len, int D, int N) {
+//
+// The gradient's registers allow two waves a SIMD and no more, so that it takes pieces of several
+// segments, and only what is behind the first piece has to be summarised.
+SsmSplit ssm_split(bool backward, const int* cu, int n, int T, int D, int N) {
   const int ch = N <= 16 ? 16 : 4;  // channels of a wave
   const int64_t per_seg = (D + ch - 1) / ch;
-  const int round = (max_len + kSsmBlock - 1) / kSsmBlock * kSsmBlock;
-  if (per_seg * nseq >= 2048 || max_len <= 4 * kSsmBlock) return round;
-  const int64_t want = (8192 + per_seg - 1) / per_seg;  // segments in all
-  int64_t seg = (rows + want - 1) / want;
-  seg = (seg + kSsmBlock - 1) / kSsmBlock * kSsmBlock;
-  if (seg < 4 * kSsmBlock) seg = 4 * kSsmBlock;
-  return seg >= round ? round : (int)seg;
+  int longest = cu ? 1 : T;
+  for (int i = 0; cu && i < n; ++i) longest = cu[i + 1] - cu[i] > longest ? cu[i + 1] - cu[i] : longest;
+  const int64_t rows = cu ? cu[n] : (int64_t)n * T;
+  auto whole = [](int64_t x, int64_t m) { return (x + m - 1) / m * m; };
+  // tokens a segment for so many waves in all
+  auto tokens = [&](int64_t waves) {
+    const int64_t want = (waves + per_seg - 1) / per_seg;
+    return whole((rows + want - 1) / want, kSsmBlock);
+  };
+  const int64_t uncut = whole(longest, kSsmBlock);
+  int64_t seg = uncut, main = uncut;
+  if (per_seg * n < 2048 && longest > 4 * kSsmBlock) {
+    seg = tokens(8192) < 4 * kSsmBlock ? 4 * kSsmBlock : tokens(8192);
+    seg = seg < uncut ? seg : uncut;
+    main = seg == uncut ? uncut : backward ? whole(tokens(2048), seg) : seg;
+  }
+  SsmSplit r{(int)seg, 0, (int)main, 0};
+  for (int i = 0; i < (cu ? n : 1); ++i) {
+    const int64_t len = cu ? cu[i + 1] - cu[i] : T, times = cu ? 1 : n;
+    r.nseg += (int)(times * ((len + seg - 1) / seg));
+    r.nmain += (int)(times * ((len + main - 1) / main));
+  }
+  return r;
 }
 
-size_t ssm_fwd_ws_bytes(int nseg, int D, int N) { return (size_t)nseg * D * (N + 1) * 4; }
+size_t ssm_fwd_ws_bytes(const SsmSplit& sp, int n, int D, int N) {
+  return sp.nseg > n ? (size_t)sp.nseg * D * (N + 1) * 4 : 0;
+}
 
 hipError_t launch_ssm_fwd(SsmParams p, int dtype, void* ws, hipStream_t st) {
-  const bool split = p.nseg > p.s.n;
+  const bool split = p.split.nseg > p.s.n;
   p.seg_state = split ? static_cast<float*>(ws) : nullptr;
-  p.seg_sum = split ? p.seg_state + (int64_t)p.nseg * p.D * p.N : nullptr;
+  p.seg_sum = split ? p.seg_state + (int64_t)p.split.nseg * p.D * p.N : nullptr;
   return ssm_dispatch(dtype, p.N, [&](auto t, auto ln, auto npl) {
     using T = decltype(t);
     constexpr int LN = decltype(ln)::value, NPL = decltype(npl)::value;
     const int groups = (p.D + 4 * (64 / LN) - 1) / (4 * (64 / LN));
-    const dim3 grid((unsigned)(groups * p.nseg));
+    const dim3 grid((unsigned)(groups * p.split.nseg));
     hipError_t e;
     if (split) {
       ssm_fwd_summary_kernel<T, LN, NPL><<<grid, 256, 0, st>>>(p, groups);

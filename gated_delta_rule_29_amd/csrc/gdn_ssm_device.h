@@ -159,15 +159,18 @@ __device__ __forceinline__ SeqPieces pieces_of(const Seqs& s, int seq, int len, 
   return r;
 }
 
-// What a workgroup of four waves does: a segment, 4 * 64 / LN channels of it, and this lane's part.
+// What a workgroup of four waves does: a segment of len tokens, 4 * 64 / LN channels of it, and this lane's part.
 template <int LN>
 struct Place {
   static constexpr int CH = 64 / LN;
   int lane, wv, j, seg, grp, c, cc, t0, t1;
   bool cv;  // the lane has a channel (loads of a lane without one read the last channel's)
   Piece pc;
-  __device__ __forceinline__ Place(const SsmParams& p, int groups) {
-    const int bid = xcd_contiguous(blockIdx.x, gridDim.x);
+  __device__ __forceinline__ Place(const SsmParams& p, int groups, int len) {
+    // Four lanes a channel: a workgroup's 64 channels are whole cache lines, and the segments that a
+    // summary leaves out are spread over the XCDs (in contiguous stretches they left half of
+    // them idle).  16 lanes: neighbours share lines and belong on one XCD.
+    const int bid = LN == 4 ? blockIdx.x : xcd_contiguous(blockIdx.x, gridDim.x);
     lane = threadIdx.x & 63;
     wv = threadIdx.x >> 6;
     j = lane % LN;
@@ -176,9 +179,9 @@ struct Place {
     c = (grp * 4 + wv) * CH + lane / LN;
     cv = c < p.D;
     cc = cv ? c : p.D - 1;
-    pc = uniform(find_piece(p.s, seg, p.seg, lane));
-    t0 = pc.begin + pc.k * p.seg;
-    t1 = min(t0 + p.seg, pc.end);
+    pc = uniform(find_piece(p.s, seg, len, lane));
+    t0 = pc.begin + pc.k * len;
+    t1 = min(t0 + len, pc.end);
   }
 };
 

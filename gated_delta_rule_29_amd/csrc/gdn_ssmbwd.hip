@@ -124,8 +124,8 @@ __global__ __launch_bounds__(256) void ssm_bwd_summary_kernel(SsmBwdParams p, in
   constexpr int NP = LN * NPL, TL = kSsmChunk / LN;
   __shared__ __align__(16) float bc[kSsmChunk * NP * 2];
   const SsmParams& f = p.f;
-  const Place<LN> w(f, groups);
-  if (w.pc.seq < 0 || w.pc.k == 0) return;  // nothing is before the first segment
+  const Place<LN> w(f, groups, f.split.seg);
+  if (w.pc.seq < 0 || w.pc.k < f.split.main / f.split.seg) return;  // nothing is before the first piece
   const int j = w.j, cc = w.cc, t0 = w.t0, t1 = w.t1;
   float A2[NPL], g[NPL] = {};
   load_decay<NPL>(f, cc, j, A2);
@@ -162,21 +162,23 @@ __global__ __launch_bounds__(256) void ssm_bwd_summary_kernel(SsmBwdParams p, in
   if (w.cv && j == 0) f.seg_sum[(int64_t)w.seg * f.D + w.c] = dsum;
 }
 
-// A sequence's segments from the last to the first: seg_state becomes the gradient that reaches each
-// segment's last state from behind it.
+// A sequence's segments from the last to the last one of its first piece: seg_state becomes the
+// gradient that reaches each segment's last state from behind it.
 __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(SsmBwdParams p, int per_seq) {
   const SsmParams& f = p.f;
   const int seq = blockIdx.x / per_seq;
   const int64_t e = (int64_t)(blockIdx.x - seq * per_seq) * 256 + threadIdx.x;
   const int64_t DN = (int64_t)f.D * f.N;
-  const SeqPieces sp = pieces_of(f.s, seq, f.seg, threadIdx.x & 63);
+  const SeqPieces sp = pieces_of(f.s, seq, f.split.seg, threadIdx.x & 63);
   if (e >= DN) return;
   const int64_t d = e / f.N;
   const float a = f.A[e] * kLog2e;
   float g = p.dht ? p.dht[seq * DN + e] : 0.f;
-  for (int i = sp.count - 1; i >= 0; --i) {
+  const int first = f.split.main / f.split.seg;
+  for (int i = sp.count - 1; i >= first - 1 && i >= 0; --i) {
     const int64_t s = sp.first + i;
-    const float own = i ? f.seg_state[s * DN + e] : 0.f, sum = i ? f.seg_sum[s * f.D + d] : 0.f;
+    const bool summed = i >= first;
+    const float own = summed ? f.seg_state[s * DN + e] : 0.f, sum = summed ? f.seg_sum[s * f.D + d] : 0.f;
     f.seg_state[s * DN + e] = g;
     g = __builtin_fmaf(__builtin_amdgcn_exp2f(a * sum), g, own);
   }
@@ -189,7 +191,7 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
   __shared__ __align__(16) float red[2][4][kSsmChunk * 2 * NP];
   __shared__ __align__(16) float shares[4][AddChannels<LN, NPL>::LDS];
   const SsmParams& f = p.f;
-  const Place<LN> w(f, groups);
+  const Place<LN> w(f, groups, f.split.main);
   if (w.pc.seq < 0) return;
   const int j = w.j, c = w.c, cc = w.cc, t0 = w.t0, t1 = w.t1;
   const bool cv = w.cv, gate = f.z;
@@ -207,7 +209,8 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
 
   float A2[NPL], g[NPL], dA[NPL] = {};
   load_decay<NPL>(f, cc, j, A2);
-  load_state<NPL>(f.seg_state ? f.seg_state + w.seg * DN : p.dht ? p.dht + w.pc.seq * DN : nullptr, cc, j, f.N, g);
+  const int64_t last_seg = find_piece_before(f.s, w.pc, f.split.seg, w.lane) + (t1 - 1 - w.pc.begin) / f.split.seg;
+  load_state<NPL>(f.seg_state ? f.seg_state + last_seg * DN : p.dht ? p.dht + w.pc.seq * DN : nullptr, cc, j, f.N, g);
   if (!cv) {  // lanes without a channel give nothing to the sums over channels
 #pragma unroll
     for (int i = 0; i < NPL; ++i) g[i] = 0.f;
@@ -353,26 +356,26 @@ size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 struct BwdWs {
   size_t state, sum, bc, a, total;
 };
-BwdWs bwd_ws(int nseg, int rows, int D, int N) {
+BwdWs bwd_ws(const SsmSplit& sp, int rows, int D, int N) {
   BwdWs w;
   const size_t groups = (D + bwd_channels(N) - 1) / bwd_channels(N);
   w.state = 0;
-  w.sum = al256((size_t)nseg * D * N * 4);
-  w.bc = w.sum + al256((size_t)nseg * D * 4);
+  w.sum = al256((size_t)sp.nseg * D * N * 4);
+  w.bc = w.sum + al256((size_t)sp.nseg * D * 4);
   w.a = w.bc + al256(groups * rows * 2 * N * 4);
-  w.total = w.a + al256((size_t)nseg * D * (N + 2) * 4);
+  w.total = w.a + al256((size_t)sp.nmain * D * (N + 2) * 4);
   return w;
 }
 
 }  // namespace
 
-size_t ssm_bwd_ws_bytes(int nseg, int rows, int D, int N) { return bwd_ws(nseg, rows, D, N).total; }
+size_t ssm_bwd_ws_bytes(const SsmSplit& sp, int rows, int D, int N) { return bwd_ws(sp, rows, D, N).total; }
 
 hipError_t launch_ssm_bwd(SsmBwdParams p, int dtype, void* ws, hipStream_t st) {
   SsmParams& f = p.f;
-  const BwdWs w = bwd_ws(f.nseg, f.s.rows, f.D, f.N);
+  const BwdWs w = bwd_ws(f.split, f.s.rows, f.D, f.N);
   char* base = static_cast<char*>(ws);
-  const bool split = f.nseg > f.s.n;
+  const bool split = f.split.nmain > f.s.n;  // (a sequence of one piece needs no summary)
   f.seg_state = split ? reinterpret_cast<float*>(base + w.state) : nullptr;
   f.seg_sum = split ? reinterpret_cast<float*>(base + w.sum) : nullptr;
   p.part_bc = reinterpret_cast<float*>(base + w.bc);
@@ -381,25 +384,21 @@ hipError_t launch_ssm_bwd(SsmBwdParams p, int dtype, void* ws, hipStream_t st) {
     using T = decltype(t);
     constexpr int LN = decltype(ln)::value, NPL = decltype(npl)::value;
     const int ch = 4 * (64 / LN), groups = (f.D + ch - 1) / ch;
-    const dim3 grid((unsigned)(groups * f.nseg));
     hipError_t e;
     if (split) {
-      ssm_bwd_summary_kernel<T, LN, NPL><<<grid, 256, 0, st>>>(p, groups);
+      ssm_bwd_summary_kernel<T, LN, NPL><<<dim3((unsigned)(groups * f.split.nseg)), 256, 0, st>>>(p, groups);
       if ((e = hipGetLastError()) != hipSuccess) return e;
       const int per_seq = (int)(((int64_t)f.D * f.N + 255) / 256);
       ssm_bwd_join_kernel<<<dim3((unsigned)(per_seq * f.s.n)), 256, 0, st>>>(p, per_seq);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    ssm_bwd_kernel<T, LN, NPL><<<grid, 256, 0, st>>>(p, groups);
+    ssm_bwd_kernel<T, LN, NPL><<<dim3((unsigned)(groups * f.split.nmain)), 256, 0, st>>>(p, groups);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     int64_t cols = (int64_t)f.s.rows * 2 * f.N;
-    column_sum_kernel<<<dim3((unsigned)((cols + 63) / 64)), 1024, 0, st>>>(
-        p.part_bc, groups, cols, BcOut<T>{static_cast<T*>(p.dB), static_cast<T*>(p.dC), f.N});
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    e = column_sum(p.part_bc, groups, cols, BcOut<T>{static_cast<T*>(p.dB), static_cast<T*>(p.dC), f.N}, st);
+    if (e != hipSuccess) return e;
     cols = (int64_t)f.D * (f.N + 2);
-    column_sum_kernel<<<dim3((unsigned)((cols + 63) / 64)), 1024, 0, st>>>(
-        p.part_a, f.nseg, cols, ParamOut{p.dA, p.dskip, p.ddt_bias, f.N});
-    return hipGetLastError();
+    return column_sum(p.part_a, f.split.nmain, cols, ParamOut{p.dA, p.dskip, p.ddt_bias, f.N}, st);
   });
 }
 
