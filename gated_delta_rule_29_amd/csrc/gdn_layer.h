@@ -95,6 +95,7 @@ struct SsmParams {
   void* y;              // [rows, D]
   float* ht;            // [n, D, N] or nullptr
   float* h;             // saved states [chunks, D, N] or nullptr
+  int64_t chunks;
   Seqs s;
   int D, N;
   bool softplus;

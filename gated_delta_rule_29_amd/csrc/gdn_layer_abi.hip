@@ -140,13 +140,15 @@ bool sizable(const int* cu, int n, int D, int N) {
   return true;
 }
 
-gdn::SsmParams scan_params(const gdn::Seqs& s, const Split& sp, const Scan& a, int D, int N, int softplus) {
+gdn::SsmParams scan_params(const gdn::Seqs& s, const Split& sp, const int* cu_host, const Scan& a, int D, int N,
+                           int softplus) {
   gdn::SsmParams p{};
   p.x = a.x; p.dt = a.dt; p.z = a.z; p.Bm = a.Bm; p.Cm = a.Cm;
   p.x_pitch = a.x_pitch; p.dt_pitch = a.dt_pitch; p.z_pitch = a.z_pitch;
   p.b_pitch = a.b_pitch; p.c_pitch = a.c_pitch;
   p.A = a.A; p.skip = a.skip; p.dt_bias = a.dt_bias;
   p.s = s; p.D = D; p.N = N; p.softplus = softplus != 0; p.split = sp;
+  p.chunks = cu_host ? ssm_scan_num_chunks(cu_host, s.n) : (int64_t)s.n * ((s.T + GDN_SSM_CHUNK - 1) / GDN_SSM_CHUNK);
   return p;
 }
 
@@ -156,7 +158,7 @@ int check_scan_grid(const gdn::Seqs& s, const Split& sp, int D, int N) {
   return check_grid(s.n, ((int64_t)D * N + 255) / 256, "ssm_scan");
 }
 
-int scan_fwd(const gdn::Seqs& s, const Split& sp, const Scan& a, const float* h0, void* y, float* ht,
+int scan_fwd(const gdn::Seqs& s, const Split& sp, const int* cu_host, const Scan& a, const float* h0, void* y, float* ht,
              float* h, int D, int N, int softplus, int dtype, void* ws, size_t ws_bytes, void* stream) {
   if (!y) return fail(GDN_ERR_INVALID, "y must be a non-null device pointer");
   GDN_TRY(check_state("h0", h0, N));
@@ -164,7 +166,7 @@ int scan_fwd(const gdn::Seqs& s, const Split& sp, const Scan& a, const float* h0
   GDN_TRY(check_state("h", h, N));
   GDN_TRY(check_scan_grid(s, sp, D, N));
   GDN_TRY(check_workspace(ws, ws_bytes, gdn::ssm_fwd_ws_bytes(sp, s.n, D, N)));
-  gdn::SsmParams p = scan_params(s, sp, a, D, N, softplus);
+  gdn::SsmParams p = scan_params(s, sp, cu_host, a, D, N, softplus);
   p.h0 = h0; p.y = y; p.ht = ht; p.h = h;
   const hipError_t e = gdn::launch_ssm_fwd(p, dtype, ws, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "ssm_scan_fwd launch");
@@ -175,7 +177,7 @@ struct ScanGrads {
   float *dA, *dskip, *ddt_bias, *dh0;
 };
 
-int scan_bwd(const gdn::Seqs& s, const Split& sp, const Scan& a, const void* dy, int64_t dy_pitch,
+int scan_bwd(const gdn::Seqs& s, const Split& sp, const int* cu_host, const Scan& a, const void* dy, int64_t dy_pitch,
              const float* h, const float* dht, const ScanGrads& o, int D, int N, int softplus, int dtype,
              void* ws, size_t ws_bytes, void* stream) {
   if (!dy || !h) return fail(GDN_ERR_INVALID, "dy and h must be non-null device pointers");
@@ -190,7 +192,7 @@ int scan_bwd(const gdn::Seqs& s, const Split& sp, const Scan& a, const void* dy,
   GDN_TRY(check_grid(s.rows, (2 * N + 63) / 64, "ssm_scan_bwd"));
   GDN_TRY(check_workspace(ws, ws_bytes, gdn::ssm_bwd_ws_bytes(sp, s.rows, D, N)));
   gdn::SsmBwdParams p{};
-  p.f = scan_params(s, sp, a, D, N, softplus);
+  p.f = scan_params(s, sp, cu_host, a, D, N, softplus);
   p.f.h = const_cast<float*>(h);
   p.dy = dy; p.dy_pitch = dy_pitch; p.dht = dht;
   p.dx = o.dx; p.ddt = o.ddt; p.dz = o.dz; p.dB = o.dBm; p.dC = o.dCm;
@@ -320,7 +322,7 @@ int ssm_scan_fwd(const void* x, int64_t x_pitch, const void* dt, int64_t dt_pitc
   gdn::Seqs s;
   GDN_TRY(check_scan(a, D, N, dtype));
   GDN_TRY(dense_seqs(B, T, &s));
-  return scan_fwd(s, dense_split(false, B, T, D, N), a, h0, y, ht, h, D, N, softplus, dtype, workspace,
+  return scan_fwd(s, dense_split(false, B, T, D, N), nullptr, a, h0, y, ht, h, D, N, softplus, dtype, workspace,
                   workspace_bytes, stream);
 }
 
@@ -333,7 +335,7 @@ int ssm_scan_fwd_varlen(const void* x, int64_t x_pitch, const void* dt, int64_t 
   gdn::Seqs s;
   GDN_TRY(check_scan(a, D, N, dtype));
   GDN_TRY(packed_seqs(cu_seqlens, cu_seqlens_host, N_seq, T_total, &s));
-  return scan_fwd(s, packed_split(false, cu_seqlens_host, N_seq, D, N), a, h0, y, ht, h, D, N, softplus, dtype,
+  return scan_fwd(s, packed_split(false, cu_seqlens_host, N_seq, D, N), cu_seqlens_host, a, h0, y, ht, h, D, N, softplus, dtype,
                   workspace, workspace_bytes, stream);
 }
 
@@ -348,7 +350,7 @@ int ssm_scan_bwd(const void* dy, int64_t dy_pitch, const float* h, const void* x
   gdn::Seqs s;
   GDN_TRY(check_scan(a, D, N, dtype));
   GDN_TRY(dense_seqs(B, T, &s));
-  return scan_bwd(s, dense_split(true, B, T, D, N), a, dy, dy_pitch, h, dht, o, D, N, softplus, dtype, workspace,
+  return scan_bwd(s, dense_split(true, B, T, D, N), nullptr, a, dy, dy_pitch, h, dht, o, D, N, softplus, dtype, workspace,
                   workspace_bytes, stream);
 }
 
@@ -364,7 +366,7 @@ int ssm_scan_bwd_varlen(const void* dy, int64_t dy_pitch, const float* h, const 
   gdn::Seqs s;
   GDN_TRY(check_scan(a, D, N, dtype));
   GDN_TRY(packed_seqs(cu_seqlens, cu_seqlens_host, N_seq, T_total, &s));
-  return scan_bwd(s, packed_split(true, cu_seqlens_host, N_seq, D, N), a, dy, dy_pitch, h, dht, o, D, N, softplus,
+  return scan_bwd(s, packed_split(true, cu_seqlens_host, N_seq, D, N), cu_seqlens_host, a, dy, dy_pitch, h, dht, o, D, N, softplus,
                   dtype, workspace, workspace_bytes, stream);
 }
 

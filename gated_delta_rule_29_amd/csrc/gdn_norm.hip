@@ -123,7 +123,7 @@ template <typename T, typename RT, int V, int TPR, int NV, int Q8>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormParams p) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
   __shared__ float red[RPW * (TPR / 64)];
-  __shared__ unsigned bmax[Q8 == 2 && V == 1 && TPR > 64 ? kNormMaxD / kBlock : 1];
+  __shared__ unsigned half[Q8 == 2 && V == 1 && TPR > 64 ? kNormMaxD / 64 + 1 : 1];  // maxima of 64 columns
   const int sub = threadIdx.x / TPR, tid = threadIdx.x % TPR;
   const int row = blockIdx.x * RPW + sub;
   if (TPR == 64 && row >= p.M) return;  // (one row a workgroup otherwise)
@@ -155,10 +155,6 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormPar
   const float r = 1.f / sqrtf(ss / (float)p.D + p.eps);
   if (p.rstd && tid == 0) p.rstd[row] = r;
   unsigned amax = 0;
-  if constexpr (Q8 == 2 && V == 1 && TPR > 64) {
-    for (int i = tid; i < (p.D + kBlock - 1) / kBlock; i += TPR) bmax[i] = 0;
-    __syncthreads();
-  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * TPR + tid) * V;
@@ -185,9 +181,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormPar
           store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[i], 1.f / s);
         }
       } else if constexpr (TPR > 64) {
-        // a wave holds half a block; a maximum does not depend on the order
-        m = wave_max(m);
-        if ((tid & 63) == 0 && c < p.D) atomicMax(&bmax[c / kBlock], m);
+        m = wave_max(m);  // a wave holds half a block
+        if ((tid & 63) == 0 && c < p.D) half[c / 64] = m;
       }
     }
   }
@@ -217,13 +212,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormPar
     }
   }
   if constexpr (Q8 == 2 && V == 1 && TPR > 64) {
+    const int nb = (p.D + kBlock - 1) / kBlock, last = (p.D - 1) / 64;
     __syncthreads();
-    const int nb = (p.D + kBlock - 1) / kBlock;
-    for (int i = tid; i < nb; i += TPR) p.scale[(int64_t)row * nb + i] = scale_of(bmax[i]);
+    auto scale = [&](int b) { return scale_of(max(half[2 * b], half[min(2 * b + 1, last)])); };
+    for (int i = tid; i < nb; i += TPR) p.scale[(int64_t)row * nb + i] = scale(i);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * TPR + tid;
-      if (c < p.D) store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[i], 1.f / scale_of(bmax[c / kBlock]));
+      if (c < p.D) store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[i], 1.f / scale(c / kBlock));
     }
   }
 }

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(256) void ssm_fwd_summary_kernel(SsmParams p, int g
         float b[NPL], cf[NPL];
         read_bc<NPL>(bc + ((g * LN + k()) * NP + j * NPL) * 2, b, cf);
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dk * A2[i]), h[i], xk * b[i]);
+        for (int i = 0; i < NPL; ++i) h[i] = __builtin_fmaf(decay(dk, A2[i]), h[i], xk * b[i]);
       });
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -91,8 +91,7 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
   load_decay<NPL>(p, cc, j, A2);
   load_state<NPL>(p.seg_state ? p.seg_state + w.seg * DN : p.h0 ? p.h0 + w.pc.seq * DN : nullptr, cc, j, p.N, h);
   const float bias = p.dt_bias ? p.dt_bias[cc] : 0.f, skip = p.skip ? p.skip[cc] : 0.f;
-  float* save = nullptr;
-  if (p.h) save = p.h + (find_piece_before(p.s, w.pc, kSsmChunk, w.lane) + (w.t0 - w.pc.begin) / kSsmChunk) * DN;
+  int64_t chunk = p.h ? find_piece_before(p.s, w.pc, kSsmChunk, w.lane) + (w.t0 - w.pc.begin) / kSsmChunk : 0;
   const unsigned vy = w.cv ? (unsigned)(j * p.D + w.c) * sizeof(T) : kNowhere;
 
   for (int tb = w.t0; tb < t1; tb += kSsmChunk) {
@@ -111,10 +110,8 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
     __syncthreads();
     st.store(bc);
     __syncthreads();
-    if (save) {
-      if (w.cv) store_state<NPL>(save, w.c, j, p.N, h);
-      save += DN;
-    }
+    if (p.h && w.cv && chunk < p.chunks) store_state<NPL>(p.h + chunk * DN, w.c, j, p.N, h);
+    ++chunk;
 #pragma unroll
     for (int g = 0; g < TL; ++g) {
       const float x = of_bits<T>(xr[g]), z = of_bits<T>(zr[g]);
@@ -131,7 +128,7 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
         float acc = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-          h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dk * A2[i]), h[i], xk * b[i]);
+          h[i] = __builtin_fmaf(decay(dk, A2[i]), h[i], xk * b[i]);
           acc = __builtin_fmaf(cf[i], h[i], acc);
         }
         yp[k()] = acc;
@@ -152,7 +149,7 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmParams p, int per_seq)
   const int64_t e = (int64_t)(blockIdx.x - seq * per_seq) * 256 + threadIdx.x;
   const int lane = threadIdx.x & 63;
   const int64_t DN = (int64_t)p.D * p.N;
-  const SeqPieces sp = pieces_of(p.s, seq, p.split.seg, lane);
+  const SeqPieces sp = pieces_of(p.s, seq, p.split.seg, p.split.nseg, lane);
   if (e >= DN) return;
   const int64_t d = e / p.N;
   const float a = p.A[e] * kLog2e;
@@ -212,7 +209,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmStepParams p, int grou
     float acc = 0.f;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      h[u][i] = __builtin_fmaf(__builtin_amdgcn_exp2f(de * (A2[u][i] * kLog2e)), h[u][i], dx * bn[i]);
+      h[u][i] = __builtin_fmaf(decay(de, A2[u][i] * kLog2e), h[u][i], dx * bn[i]);
       acc = __builtin_fmaf(cn[i], h[u][i], acc);
     }
     const float s = z[u] * sigmoid_f(z[u]);

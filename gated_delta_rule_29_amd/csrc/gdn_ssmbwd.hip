@@ -152,7 +152,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_summary_kernel(SsmBwdParams p, in
         read_bc<NPL>(bc + ((q * LN + k) * NP + j * NPL) * 2, b, cf);
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
-          g[i] = __builtin_fmaf(cf[i], gk, g[i]) * __builtin_amdgcn_exp2f(dk * A2[i]);
+          g[i] = __builtin_fmaf(cf[i], gk, g[i]) * decay(dk, A2[i]);
       });
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(SsmBwdParams p, int p
   const int seq = blockIdx.x / per_seq;
   const int64_t e = (int64_t)(blockIdx.x - seq * per_seq) * 256 + threadIdx.x;
   const int64_t DN = (int64_t)f.D * f.N;
-  const SeqPieces sp = pieces_of(f.s, seq, f.split.seg, threadIdx.x & 63);
+  const SeqPieces sp = pieces_of(f.s, seq, f.split.seg, f.split.nseg, threadIdx.x & 63);
   if (e >= DN) return;
   const int64_t d = e / f.N;
   const float a = f.A[e] * kLog2e;
@@ -202,14 +202,15 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
   ChunkIn<T, LN> in;
   StageBC<T, NP, kSsmChunk, 256> st;
   float hs[NPL];
-  const float* saved = f.h + (find_piece_before(f.s, w.pc, kSsmChunk, w.lane) + (tb - w.pc.begin) / kSsmChunk) * DN;
+  int64_t chunk = min(find_piece_before(f.s, w.pc, kSsmChunk, w.lane) + (tb - w.pc.begin) / kSsmChunk, f.chunks - 1);
   in.ask(p, tb, min(t1 - tb, kSsmChunk), j, cc);
   st.load(f, tb, min(t1 - tb, kSsmChunk));
-  load_state<NPL>(saved, cc, j, f.N, hs);
+  load_state<NPL>(f.h + chunk * DN, cc, j, f.N, hs);
 
   float A2[NPL], g[NPL], dA[NPL] = {};
   load_decay<NPL>(f, cc, j, A2);
-  const int64_t last_seg = find_piece_before(f.s, w.pc, f.split.seg, w.lane) + (t1 - 1 - w.pc.begin) / f.split.seg;
+  const int64_t last_seg =
+      min(find_piece_before(f.s, w.pc, f.split.seg, w.lane) + (t1 - 1 - w.pc.begin) / f.split.seg, (int64_t)f.split.nseg - 1);
   load_state<NPL>(f.seg_state ? f.seg_state + last_seg * DN : p.dht ? p.dht + w.pc.seq * DN : nullptr, cc, j, f.N, g);
   if (!cv) {  // lanes without a channel give nothing to the sums over channels
 #pragma unroll
@@ -244,7 +245,7 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
         read_bc<NPL>(bc[buf] + ((q * LN + k()) * NP + j * NPL) * 2, b, cf);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-          const float e = __builtin_amdgcn_exp2f(dk * A2[i]);
+          const float e = decay(dk, A2[i]);
           a[q * LN + k()][i] = e;
           ah[q * LN + k()][i] = e * h[i];
           h[i] = __builtin_fmaf(xk, b[i], e * h[i]);
@@ -258,10 +259,10 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
     for (int q = TL - 1; q >= 0; --q) {
       if (q == (TL > 1 ? TL - 2 : 0)) {  // the next chunk's inputs, once the last group's a and a h are done with
         const int left = more ? kSsmChunk : 0;
-        saved -= more ? DN : 0;
+        chunk -= more && chunk > 0;
         in.ask(p, tb - kSsmChunk, left, j, cc);
         st.load(f, tb - kSsmChunk, left);
-        load_state<NPL>(saved, cc, j, f.N, hs);
+        load_state<NPL>(f.h + chunk * DN, cc, j, f.N, hs);
       }
       const float dx = tk[q].de * x[q];
       float yv[LN], gb[LN], ga[LN];

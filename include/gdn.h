@@ -642,6 +642,7 @@ GDN_API int gdn_bwd_dhu_varlen(const void* q, const void* k, const void* w, cons
  *    multiples of 16 bytes) is faster.  fp32 [.., D, N] tensors (A, states) must be 16-byte
  *    aligned where N is a multiple of 4.
  *  - Sums over rows and channels are joined in a fixed order: results are deterministic.
+ *  - Outputs must not overlap inputs (a step's state excepted).
  * ------------------------------------------------------------------------------------------ */
 
 /*
@@ -703,7 +704,7 @@ GDN_API int causal_conv_step(const void* x, int64_t x_pitch, const float* w, con
  *     h_t[d,n] = e^{de_t[d] A[d,n]} h_{t-1}[d,n] + de_t[d] x_t[d] Bm_t[n]
  *     y_t[d] = (sum_n Cm_t[n] h_t[d,n] + skip[d] x_t[d]) * (z ? z_t[d] sigmoid(z_t[d]) : 1)
  *   x, dt, z  [B, T, D] (a pitch each; z NULL: no gate)
- *   A         [D, N] fp32 (natural; negative for a decay)
+ *   A         [D, N] fp32 (natural; negative for a decay; finite)
  *   Bm, Cm    [B, T, N] (a pitch each), shared by all channels
  *   skip, dt_bias [D] fp32 or NULL (0);  h0 [B, D, N] fp32 or NULL (0)
  *   y  [B, T, D] OUT;  ht [B, D, N] fp32 OUT or NULL: the state after the last token

@@ -27,12 +27,13 @@ CASES = [
 
 
 def _inputs(lens, dense, D, N, pitch, dtype, seed):
+    """Step sizes between about 1e-4 and 0.3: some states last a few tokens, others some thousands."""
     g = gen(seed)
     lead, cu = rows(lens, dense)
     t, n = TYPES[dtype], len(lens)
     A = -torch.arange(1, N + 1).float() * torch.exp(0.3 * rn(g, D, N))
-    c = dict(x=rn(g, *lead, D, dtype=t), dt=(rn(g, *lead, D) - 1.0).to(t), A=A, Bm=rn(g, *lead, N, dtype=t),
-             Cm=rn(g, *lead, N, dtype=t), skip=rn(g, D), z=rn(g, *lead, D, dtype=t), dt_bias=0.5 * rn(g, D),
+    c = dict(x=rn(g, *lead, D, dtype=t), dt=(rn(g, *lead, D) - 3.0).to(t), A=A, Bm=rn(g, *lead, N, dtype=t),
+             Cm=rn(g, *lead, N, dtype=t), skip=rn(g, D), z=rn(g, *lead, D, dtype=t), dt_bias=-4 * torch.rand(D, generator=g),
              h0=rn(g, n, D, N), dy=rn(g, *lead, D, dtype=t), dht=rn(g, n, D, N))
     d = {k: v.to(DEV) for k, v in c.items()}
     if pitch[0]:
@@ -84,7 +85,7 @@ def test_plain_step_sizes(dtype):
     say("scan without softplus %s" % dtype)
     c, d, _ = _inputs([50, 50], True, 34, 16, (0, 0), dtype, 77)
     for k in (c, d):
-        k["dt"] = torch.clamp(k["dt"], min=0.0)
+        k["dt"] = torch.clamp(0.1 * (k["dt"] + 3.0), min=0.0)
     args = (d["x"], d["dt"], d["A"], d["Bm"], d["Cm"])
     out = g.ssm_scan_fwd(*args, softplus=False, want_h=True)
     ref = _ref(c, False)
@@ -201,3 +202,87 @@ def test_split_sequences_agree_with_whole_ones():
         h = o["ht"]
     check("y", whole["y"][0], arr(torch.cat(ys, 1)[0]))
     check("ht", whole["ht"], arr(h))
+
+
+def test_cut_gradient_agrees_with_pieces():
+    """A sequence long and wide enough that the gradient takes pieces of several segments (1040 channels,
+    8155 tokens), against the same tokens in calls of 96 that are never cut, chained by their states
+    and state gradients: equal up to fp32 rounding.
+
+    How far two fp32 results may be apart here: states last up to M = 1000 tokens (step sizes of 1e-3), so to
+    the 40 roundings of one result come M decays, each off by 0.6 u (u = 2^-24) at random (0.31 the
+    exponential, half an ulp the recurrence) and by less than 0.03 u in the mean: 0.6 sqrt(M) + 0.03 M
+    = 49 u.  Two results: 2 * 89 u of the largest element, which is far more than 8 RMS where step
+    sizes differ a thousandfold (y's is 62)."""
+
+    def near(name, got, ref):
+        big = float(np.abs(ref).max() / np.sqrt((ref * ref).mean()))
+        check(name, got, ref, 2 * 89 * 2.0 ** -24 * big)
+
+    import gated_delta_rule_29_amd as g
+
+    say("scan gradient: cut and in pieces")
+    T, C, N, P = 8155, 1040, 16, 96
+    _, d, _ = _inputs([T], True, C, N, (0, 0), "f32", 21)
+    opt = dict(D=d["skip"], dt_bias=d["dt_bias"])
+    seqs = ("x", "dt", "Bm", "Cm", "z", "dy")
+
+    def piece(a):
+        k = {n: d[n][:, a:a + P].contiguous() for n in seqs}
+        return k, (k["x"], k["dt"], d["A"], k["Bm"], k["Cm"])
+
+    whole = (d["x"], d["dt"], d["A"], d["Bm"], d["Cm"])
+    o = g.ssm_scan_fwd(*whole, z=d["z"], h0=d["h0"], want_h=True, **opt)
+    gr = g.ssm_scan_bwd(d["dy"], o["h"], *whole, z=d["z"], dht=d["dht"], want_dh0=True, **opt)
+    h, hs, y = d["h0"], [], []
+    for a in range(0, T, P):
+        k, args = piece(a)
+        f = g.ssm_scan_fwd(*args, z=k["z"], h0=h, want_h=True, **opt)
+        h = f["ht"]
+        hs.append(f["h"])
+        y.append(f["y"])
+    near("y", o["y"], arr(torch.cat(y, 1)))
+    near("ht", o["ht"], arr(h))
+    near("h", o["h"], arr(torch.cat(hs, 1)))
+    dh, parts = d["dht"], []
+    for i, a in reversed(list(enumerate(range(0, T, P)))):
+        k, args = piece(a)
+        p = g.ssm_scan_bwd(k["dy"], hs[i], *args, z=k["z"], dht=dh, want_dh0=True, **opt)
+        dh = p["dh0"]
+        parts.insert(0, p)
+    near("dh0", gr["dh0"], arr(dh))
+    for n in ("dx", "ddt", "dB", "dC", "dz"):
+        near(n, gr[n], arr(torch.cat([p[n] for p in parts], 1)))
+    for n in ("dA", "dD", "ddt_bias"):
+        near(n, gr[n], sum(arr(p[n]) for p in parts))
+
+
+@pytest.mark.parametrize("varied,inputs,bound", [(False, 1.0, 4680), (True, 1.0, 4680), (False, 0.0, 2712),
+                                                 (True, 0.0, 212)])
+def test_states_that_last(varied, inputs, bound):
+    """4000 single tokens with step sizes of about 1e-4, so that the state keeps two thirds of itself and each
+    of its 4000 decays is rounded (u = 2^-24 of the state; 40 u for everything else):
+     - varied step sizes, no inputs: the recurrence's roundings (0.5 u sqrt(4000) = 32 u) and the decays'
+       (0.31 u sqrt(4000) = 20 u) are random, the decays' mean is below 0.03 u (120 u): 212 u in all.
+       (An exponential low by 0.115 u in the mean would be off by 460 u.)
+     - the same step size every time, no inputs: the decay is rounded the same way 4000 times, by up to the
+       exponential's 0.66 u: 2640 u, 2712 u in all, as for any recurrence whose decay is held in fp32;
+     - inputs that hold the state near its fixed point: there its own rounding repeats too, 0.5 u a token:
+       4000 * (0.66 + 0.5) u + 40 u = 4680 u, as for any recurrence whose state is held in fp32."""
+    import gated_delta_rule_29_amd as g
+
+    say("scan: states that last, varied %s inputs %s" % (varied, inputs))
+    r, C, N, steps = gen(31), 64, 4, 4000
+    dt = 1e-4 * (1 + 0.5 * torch.rand(1, C, generator=r))
+    A = -(1 + 0.01 * torch.rand(C, N, generator=r))
+    x, Bm, Cm = torch.full((1, C), inputs), torch.ones(1, N), torch.ones(1, N)
+    dts = dt * (0.5 + torch.rand(steps, C, generator=r)) if varied else dt.expand(steps, C).contiguous()
+    d = [t.to(DEV) for t in (x, dts, A, Bm, Cm)]
+    state, ref = torch.ones(1, C, N, device=DEV), torch.ones(C, N, dtype=torch.float64)
+    for i in range(steps):
+        g.ssm_step(d[0], d[1][i:i + 1], d[2], d[3], d[4], state, softplus=False)
+        e = dts[i].double()[:, None]
+        ref = torch.exp(e * A.double()) * ref + e * inputs
+    err = float(((state.cpu().double() - ref[None]).abs() / ref).max()) * 2 ** 24
+    say("  error %.1f u" % err)
+    assert err <= bound
