@@ -97,7 +97,8 @@ constexpr int dpp_row(int k) { return 0x150 + k; }
 // Value of lane k of this lane's group of LN lanes.
 template <int LN, int K>
 __device__ __forceinline__ float lane_of(float x) {
-  if constexpr (LN == 4) return dpp<dpp_quad(K)>(x);
+  if constexpr (LN == 1) return x;
+  else if constexpr (LN == 4) return dpp<dpp_quad(K)>(x);
   else return dpp<dpp_row(K)>(x);
 }
 
@@ -106,7 +107,7 @@ __device__ __forceinline__ float lane_of(float x) {
 template <int LN, int K>
 __device__ __forceinline__ float shared_lane(float x) {
   float r = lane_of<LN, K>(x);
-  asm("" : "+v"(r));  // no instruction; keeps the move from being folded into the products
+  if constexpr (LN > 1) asm("" : "+v"(r));  // no instruction; keeps the move from being folded into the products
   return r;
 }
 
@@ -115,7 +116,8 @@ __device__ __forceinline__ float shared_lane(float x) {
 // keeps that.
 template <int LN>
 __device__ __forceinline__ float reduce_scatter(const float (&v)[LN], int j) {
-  if constexpr (LN == 4) {
+  if constexpr (LN == 1) return v[0];
+  else if constexpr (LN == 4) {
     const bool b1 = j & 2, b0 = j & 1;
     const float p = (b1 ? v[2] : v[0]) + dpp<kDppXor2>(b1 ? v[0] : v[2]);
     const float q = (b1 ? v[3] : v[1]) + dpp<kDppXor2>(b1 ? v[1] : v[3]);

@@ -16,11 +16,14 @@ __device__ __forceinline__ void load_state(const float* st, int c, int j, int N,
     return;
   }
   const float* q = st + (int64_t)c * N + j * NPL;
-  if (NPL == 4 && N % 4 == 0) {
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (j * NPL < N) v = *reinterpret_cast<const f32x4*>(q);
+  if (NPL % 4 == 0 && N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) h[i] = v[i % 4];
+    for (int s = 0; s < NPL; s += 4) {
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      if (j * NPL + s < N) v = *reinterpret_cast<const f32x4*>(q + s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[(s + i) % NPL] = v[i];
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) h[i] = j * NPL + i < N ? q[i] : 0.f;
@@ -29,11 +32,12 @@ __device__ __forceinline__ void load_state(const float* st, int c, int j, int N,
 template <int NPL>
 __device__ __forceinline__ void store_state(float* st, int c, int j, int N, const float (&h)[NPL]) {
   float* q = st + (int64_t)c * N + j * NPL;
-  if (NPL == 4 && N % 4 == 0) {
-    f32x4 v;
+  if (NPL % 4 == 0 && N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = h[i % NPL];
-    if (j * NPL < N) *reinterpret_cast<f32x4*>(q) = v;
+    for (int s = 0; s < NPL; s += 4) {
+      if (j * NPL + s < N)
+        *reinterpret_cast<f32x4*>(q + s) = f32x4{h[s], h[(s + 1) % NPL], h[(s + 2) % NPL], h[(s + 3) % NPL]};
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
@@ -126,6 +130,7 @@ __device__ __forceinline__ void load_decay(const SsmParams& p, int cc, int j, fl
 // Sum over a channel's LN lanes, in each of them.
 template <int LN>
 __device__ __forceinline__ float group_sum(float x) {
+  if constexpr (LN == 1) return x;
   x += dpp<kDppXor1>(x);
   x += dpp<kDppXor2>(x);
   if constexpr (LN == 16) {

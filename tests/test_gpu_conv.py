@@ -19,6 +19,7 @@ CASES = [
     ([16, 48, 63, 1, 1, 1, 1, 129], False, 264, 2, (264, 264)),
     ([300], True, 513, 4, (1, 0)),
     ([1000, 24], False, 2056, 4, (0, 0)),
+    ([1, 2] * 600, False, 12, 3, (0, 0)),               # more sequences than are looked up in LDS
 ]
 
 
