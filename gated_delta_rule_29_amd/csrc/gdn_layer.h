@@ -6,7 +6,6 @@
 // one has its sequences' tokens in order, sequence i covering rows [cu[i], cu[i + 1]).
 #pragma once
 
-#include <stdarg.h>
 #include <stdint.h>
 
 #include <hip/hip_runtime.h>
@@ -70,7 +69,8 @@ hipError_t launch_conv_fwd(const ConvParams& p, int dtype, hipStream_t st);
 hipError_t launch_conv_bwd(const ConvBwdParams& p, int dtype, hipStream_t st);
 hipError_t launch_conv_step(const ConvStepParams& p, int dtype, hipStream_t st);
 
-// Tokens between two saved states of the selective scan, and of a step of its forward kernels.
+// Tokens between two saved states of the selective scan (and of a step of its kernels); tokens that a
+// segment's summary takes at a time, of which segments have a multiple.
 constexpr int kSsmChunk = 16;
 constexpr int kSsmBlock = 32;
 constexpr int kSsmMaxN = 64;

@@ -42,7 +42,8 @@ int check_state(const char* name, const void* p, int N) {
 // The sequences of a dense call.
 int dense_seqs(int B, int T, gdn::Seqs* s) {
   if (B <= 0 || T <= 0) return fail(GDN_ERR_INVALID, "B and T must be positive (got %d, %d)", B, T);
-  if ((int64_t)B * T > INT32_MAX) return fail(GDN_ERR_INVALID, "B*T = %lld exceeds 2^31 - 1", (long long)B * T);
+  if ((int64_t)B * T > GDN_MAX_TOKENS)
+    return fail(GDN_ERR_INVALID, "B*T = %lld exceeds %d", (long long)B * T, GDN_MAX_TOKENS);
   *s = gdn::Seqs{nullptr, B, T, B * T};
   return GDN_OK;
 }
@@ -51,6 +52,7 @@ int dense_seqs(int B, int T, gdn::Seqs* s) {
 int packed_seqs(const int* cu, const int* cu_host, int N, int T_total, gdn::Seqs* s) {
   if (!cu || !cu_host) return fail(GDN_ERR_INVALID, "cu_seqlens (device) and cu_seqlens_host must be non-null");
   if (N < 1 || T_total < 1) return fail(GDN_ERR_INVALID, "N and T_total must be positive (got %d, %d)", N, T_total);
+  if (T_total > GDN_MAX_TOKENS) return fail(GDN_ERR_INVALID, "T_total = %d exceeds %d", T_total, GDN_MAX_TOKENS);
   if (cu_host[0] != 0) return fail(GDN_ERR_INVALID, "cu_seqlens[0] must be 0 (got %d)", cu_host[0]);
   for (int i = 0; i < N; ++i)
     if (cu_host[i + 1] <= cu_host[i])
@@ -137,7 +139,7 @@ bool sizable(const int* cu, int n, int D, int N) {
   if (!cu || n < 1 || D <= 0 || N <= 0 || N > gdn::kSsmMaxN || cu[0] != 0) return false;
   for (int i = 0; i < n; ++i)
     if (cu[i + 1] <= cu[i]) return false;
-  return true;
+  return cu[n] <= GDN_MAX_TOKENS;
 }
 
 gdn::SsmParams scan_params(const gdn::Seqs& s, const Split& sp, const int* cu_host, const Scan& a, int D, int N,
@@ -217,6 +219,7 @@ int check_norm(const void* x, int64_t x_pitch, const void* residual, int64_t r_p
   if (dtype == GDN_DTYPE_F32 && rdtype != GDN_DTYPE_F32)
     return fail(GDN_ERR_UNSUPPORTED, "fp32 activations with a bf16 residual");
   if (M <= 0 || D <= 0) return fail(GDN_ERR_INVALID, "M and D must be positive (got %d, %d)", M, D);
+  if (M > GDN_MAX_TOKENS) return fail(GDN_ERR_INVALID, "M = %d exceeds %d", M, GDN_MAX_TOKENS);
   if (D > gdn::kNormMaxD) return fail(GDN_ERR_UNSUPPORTED, "D must be <= %d, got %d", gdn::kNormMaxD, D);
   if (!(eps > 0.f)) return fail(GDN_ERR_INVALID, "eps must be positive (got %g)", (double)eps);
   GDN_TRY(check_pitch("x", x, x_pitch, D));
@@ -295,7 +298,7 @@ int ssm_scan_num_chunks(const int* cu_seqlens_host, int N_seq) {
 }
 
 size_t ssm_scan_fwd_workspace_bytes(int B, int T, int D, int N) {
-  if (B <= 0 || T <= 0 || D <= 0 || N <= 0 || N > gdn::kSsmMaxN || (int64_t)B * T > INT32_MAX) return 0;
+  if (B <= 0 || T <= 0 || D <= 0 || N <= 0 || N > gdn::kSsmMaxN || (int64_t)B * T > GDN_MAX_TOKENS) return 0;
   return gdn::ssm_fwd_ws_bytes(dense_split(false, B, T, D, N), B, D, N);
 }
 
@@ -305,7 +308,7 @@ size_t ssm_scan_fwd_varlen_workspace_bytes(const int* cu_seqlens_host, int N_seq
 }
 
 size_t ssm_scan_bwd_workspace_bytes(int B, int T, int D, int N) {
-  if (B <= 0 || T <= 0 || D <= 0 || N <= 0 || N > gdn::kSsmMaxN || (int64_t)B * T > INT32_MAX) return 0;
+  if (B <= 0 || T <= 0 || D <= 0 || N <= 0 || N > gdn::kSsmMaxN || (int64_t)B * T > GDN_MAX_TOKENS) return 0;
   return gdn::ssm_bwd_ws_bytes(dense_split(true, B, T, D, N), B * T, D, N);
 }
 

@@ -97,8 +97,7 @@ constexpr int dpp_row(int k) { return 0x150 + k; }
 // Value of lane k of this lane's group of LN lanes.
 template <int LN, int K>
 __device__ __forceinline__ float lane_of(float x) {
-  if constexpr (LN == 1) return x;
-  else if constexpr (LN == 4) return dpp<dpp_quad(K)>(x);
+  if constexpr (LN == 4) return dpp<dpp_quad(K)>(x);
   else return dpp<dpp_row(K)>(x);
 }
 
@@ -107,7 +106,7 @@ __device__ __forceinline__ float lane_of(float x) {
 template <int LN, int K>
 __device__ __forceinline__ float shared_lane(float x) {
   float r = lane_of<LN, K>(x);
-  if constexpr (LN > 1) asm("" : "+v"(r));  // no instruction; keeps the move from being folded into the products
+  asm("" : "+v"(r));  // no instruction; keeps the move from being folded into the products
   return r;
 }
 
@@ -116,8 +115,7 @@ __device__ __forceinline__ float shared_lane(float x) {
 // keeps that.
 template <int LN>
 __device__ __forceinline__ float reduce_scatter(const float (&v)[LN], int j) {
-  if constexpr (LN == 1) return v[0];
-  else if constexpr (LN == 4) {
+  if constexpr (LN == 4) {
     const bool b1 = j & 2, b0 = j & 1;
     const float p = (b1 ? v[2] : v[0]) + dpp<kDppXor2>(b1 ? v[0] : v[2]);
     const float q = (b1 ? v[3] : v[1]) + dpp<kDppXor2>(b1 ? v[1] : v[3]);
@@ -220,6 +218,16 @@ __device__ __forceinline__ int seq_of_row(const Seqs& s, int t) {
 struct Piece {
   int seq, k, before, begin, end;  // begin, end: the sequence's rows
 };
+// A sequence as its one piece (seq < 0: it has no tokens).
+__device__ __forceinline__ Piece whole_sequence(const Seqs& s, int i) {
+  Piece r;
+  r.k = 0;
+  r.before = i;
+  r.begin = seq_begin(s, i);
+  r.end = seq_begin(s, i + 1);
+  r.seq = r.end > r.begin ? i : -1;
+  return r;
+}
 __device__ __forceinline__ Piece find_piece(const Seqs& s, int id, int len, int lane) {
   Piece r;
   if (!s.cu) {

@@ -27,7 +27,7 @@ template <typename T, int LN, int NPL>
 __global__ __launch_bounds__(256) void ssm_fwd_summary_kernel(SsmParams p, int groups) {
   constexpr int NP = LN * NPL, TL = kSsmBlock / LN;
   __shared__ __align__(16) float bc[kSsmBlock * NP * 2];
-  const Place<LN> w(p, groups, p.split.seg);
+  const Place<LN> w(p, groups, p.split.seg, p.split.nseg);
   if (w.pc.seq < 0 || w.t1 == w.pc.end) return;  // nothing follows the last segment
   const int j = w.j, cc = w.cc;
   float A2[NPL], h[NPL] = {};
@@ -78,7 +78,7 @@ template <typename T, int LN, int NPL>
 __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmParams p, int groups) {
   constexpr int NP = LN * NPL, TL = kSsmChunk / LN;
   __shared__ __align__(16) float bc[kSsmChunk * NP * 2];
-  const Place<LN> w(p, groups, p.split.seg);
+  const Place<LN> w(p, groups, p.split.seg, p.split.nseg);
   if (w.pc.seq < 0) return;
   const int j = w.j, cc = w.cc, t1 = w.t1;
   const bool gate = p.z;

@@ -7,7 +7,7 @@
 namespace gdn {
 
 // A lane's NPL states of channel c: st[c][j * NPL ..], zero behind the N-th and where st is null.
-// One vector access where the lanes' shares are whole (N = LN * NPL); states are 16-byte aligned.
+// One vector access where N is a multiple of a lane's four; states are 16-byte aligned then.
 template <int NPL>
 __device__ __forceinline__ void load_state(const float* st, int c, int j, int N, float (&h)[NPL]) {
   if (!st) {
@@ -16,14 +16,11 @@ __device__ __forceinline__ void load_state(const float* st, int c, int j, int N,
     return;
   }
   const float* q = st + (int64_t)c * N + j * NPL;
-  if (NPL % 4 == 0 && N % 4 == 0) {
+  if (NPL == 4 && N % 4 == 0) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (j * NPL < N) v = *reinterpret_cast<const f32x4*>(q);
 #pragma unroll
-    for (int s = 0; s < NPL; s += 4) {
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
-      if (j * NPL + s < N) v = *reinterpret_cast<const f32x4*>(q + s);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[(s + i) % NPL] = v[i];
-    }
+    for (int i = 0; i < NPL; ++i) h[i] = v[i % 4];
   } else {
 #pragma unroll
     for (int i = 0; i < NPL; ++i) h[i] = j * NPL + i < N ? q[i] : 0.f;
@@ -32,12 +29,11 @@ __device__ __forceinline__ void load_state(const float* st, int c, int j, int N,
 template <int NPL>
 __device__ __forceinline__ void store_state(float* st, int c, int j, int N, const float (&h)[NPL]) {
   float* q = st + (int64_t)c * N + j * NPL;
-  if (NPL % 4 == 0 && N % 4 == 0) {
+  if (NPL == 4 && N % 4 == 0) {
+    f32x4 v;
 #pragma unroll
-    for (int s = 0; s < NPL; s += 4) {
-      if (j * NPL + s < N)
-        *reinterpret_cast<f32x4*>(q + s) = f32x4{h[s], h[(s + 1) % NPL], h[(s + 2) % NPL], h[(s + 3) % NPL]};
-    }
+    for (int i = 0; i < 4; ++i) v[i] = h[i % NPL];
+    if (j * NPL < N) *reinterpret_cast<f32x4*>(q) = v;
   } else {
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
@@ -130,7 +126,6 @@ __device__ __forceinline__ void load_decay(const SsmParams& p, int cc, int j, fl
 // Sum over a channel's LN lanes, in each of them.
 template <int LN>
 __device__ __forceinline__ float group_sum(float x) {
-  if constexpr (LN == 1) return x;
   x += dpp<kDppXor1>(x);
   x += dpp<kDppXor2>(x);
   if constexpr (LN == 16) {
@@ -181,7 +176,8 @@ struct Place {
   int lane, wv, j, seg, grp, c, cc, t0, t1;
   bool cv;  // the lane has a channel (loads of a lane without one read the last channel's)
   Piece pc;
-  __device__ __forceinline__ Place(const SsmParams& p, int groups, int len) {
+  // total: the pieces of len tokens in all (as many as sequences where none is cut)
+  __device__ __forceinline__ Place(const SsmParams& p, int groups, int len, int total) {
     // Four lanes a channel: a workgroup's 64 channels are whole cache lines, and the segments that a
     // summary leaves out are spread over the XCDs (in contiguous stretches they left half of
     // them idle).  16 lanes: neighbours share lines and belong on one XCD.
@@ -194,7 +190,7 @@ struct Place {
     c = (grp * 4 + wv) * CH + lane / LN;
     cv = c < p.D;
     cc = cv ? c : p.D - 1;
-    pc = uniform(find_piece(p.s, seg, len, lane));
+    pc = uniform(total == p.s.n ? whole_sequence(p.s, seg) : find_piece(p.s, seg, len, lane));
     t0 = pc.begin + pc.k * len;
     t1 = min(t0 + len, pc.end);
   }

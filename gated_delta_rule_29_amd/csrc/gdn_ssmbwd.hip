@@ -124,7 +124,7 @@ __global__ __launch_bounds__(256) void ssm_bwd_summary_kernel(SsmBwdParams p, in
   constexpr int NP = LN * NPL, TL = kSsmChunk / LN;
   __shared__ __align__(16) float bc[kSsmChunk * NP * 2];
   const SsmParams& f = p.f;
-  const Place<LN> w(f, groups, f.split.seg);
+  const Place<LN> w(f, groups, f.split.seg, f.split.nseg);
   if (w.pc.seq < 0 || w.pc.k < f.split.main / f.split.seg) return;  // nothing is before the first piece
   const int j = w.j, cc = w.cc, t0 = w.t0, t1 = w.t1;
   float A2[NPL], g[NPL] = {};
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
   __shared__ __align__(16) float red[2][4][kSsmChunk * 2 * NP];
   __shared__ __align__(16) float shares[4][AddChannels<LN, NPL>::LDS];
   const SsmParams& f = p.f;
-  const Place<LN> w(f, groups, f.split.main);
+  const Place<LN> w(f, groups, f.split.main, f.split.nmain);
   if (w.pc.seq < 0) return;
   const int j = w.j, c = w.c, cc = w.cc, t0 = w.t0, t1 = w.t1;
   const bool cv = w.cv, gate = f.z;

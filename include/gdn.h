@@ -80,7 +80,8 @@ extern "C" {
 #define GDN_ERR_WORKSPACE 3   /* workspace missing or smaller than the size query returns   */
 #define GDN_ERR_HIP 4         /* a HIP launch or runtime call failed (RuntimeError)          */
 
-#define GDN_MAX_PITCH (1 << 23) /* elements from row to row of the layer operators' inputs */
+#define GDN_MAX_PITCH (1 << 23)  /* elements from row to row of the layer operators' inputs */
+#define GDN_MAX_TOKENS (1 << 30) /* tokens (rows) of one call of theirs */
 
 #define GDN_DTYPE_F32 0
 #define GDN_DTYPE_BF16 1
@@ -634,7 +635,8 @@ GDN_API int gdn_bwd_dhu_varlen(const void* q, const void* k, const void* w, cons
  *  - x [tokens, C] with a pitch: row r starts at x + r * pitch elements.  A dense batch of B
  *    sequences of T tokens has rows b * T + t; a packed batch (_varlen) has T_total rows,
  *    sequence i covering rows [cu[i], cu[i+1]), with cu_seqlens and cu_seqlens_host as in
- *    gdn_fwd_varlen.  Outputs are dense.  Pitches beyond GDN_MAX_PITCH are
+ *    gdn_fwd_varlen.  Outputs are dense.  A call has at most GDN_MAX_TOKENS rows
+ *    (GDN_ERR_INVALID); pitches beyond GDN_MAX_PITCH are
  *    GDN_ERR_UNSUPPORTED (32 rows are addressed with 32-bit offsets).
  *  - dtype is that of the activations (inputs and outputs that are not said to be fp32);
  *    all arithmetic, states and sums over tokens or channels are fp32, each result rounded once.

@@ -24,6 +24,7 @@ CASES = [
     ([333, 333], True, 12, 33, (0, 0), False),                # cut, 16 lanes a channel
     ([200], True, 1030, 16, (0, 0), True),
     ([3, 1, 130] * 40, False, 20, 16, (0, 0), True),          # more sequences than a wave has lanes
+    ([1, 2, 3] * 700, False, 16, 4, (0, 0), True),            # so many that none is cut
 ]
 
 

@@ -39,7 +39,7 @@ def test_conv_codes():
                                    a["W"], 1, a["dt"], None)
 
     for bad in (dict(x=None), dict(w=None), dict(y=None), dict(B=0), dict(T=0), dict(D=0), dict(dt=2), dict(p=7),
-                dict(W=0), dict(B=1 << 16, T=1 << 16), dict(T=1 << 30, D=1 << 20, p=1 << 20)):
+                dict(W=0), dict(B=1 << 16, T=1 << 16), dict(T=(1 << 30) + 1), dict(T=1 << 30, D=1 << 20, p=1 << 20)):
         assert fwd(**bad) == L.ERR_INVALID, bad
     assert fwd(W=1) == L.ERR_UNSUPPORTED and fwd(W=5) == L.ERR_UNSUPPORTED
 
@@ -147,7 +147,7 @@ def test_step_and_norm_codes():
                                 a["D"], a["dt"], a["rt"], None)
 
     for bad in (dict(x=None), dict(w=None), dict(y=None), dict(xp=7), dict(r=FAKE, rp=7), dict(eps=0.0),
-                dict(eps=float("nan")), dict(M=0), dict(D=0), dict(dt=2), dict(rt=2), dict(s=FAKE)):
+                dict(eps=float("nan")), dict(M=0), dict(M=(1 << 30) + 1), dict(D=0), dict(dt=2), dict(rt=2), dict(s=FAKE)):
         assert norm(**bad) == L.ERR_INVALID, bad
     assert norm(dt=0, rt=1) == L.ERR_UNSUPPORTED and norm(D=32769, xp=32769) == L.ERR_UNSUPPORTED
 
