@@ -25,34 +25,35 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _bad(t, name, shape, dtype, dev):
+def _refuse(t, name, shape, dtype, dev, why):
+    """Says what is wrong with a tensor that failed a check: why, unless it is its kind or shape."""
     if not isinstance(t, torch.Tensor):
-        return "%s must be a torch.Tensor" % name
-    if t.shape != shape:
-        return "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape))
-    if t.dtype != dtype:
-        return "%s has dtype %s, expected %s" % (name, t.dtype, dtype)
-    if t.device != dev:
-        return "%s is on %s, expected %s" % (name, t.device, dev)
-    return None
+        why = "%s must be a torch.Tensor" % name
+    elif t.shape != shape:
+        why = "%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape))
+    elif t.dtype != dtype:
+        why = "%s has dtype %s, expected %s" % (name, t.dtype, dtype)
+    elif t.device != dev:
+        why = "%s is on %s, expected %s" % (name, t.device, dev)
+    raise ValueError(why)
 
+
+# The checks are written out: single-token calls are bound by the time that they take on the host.
 
 def _need(t, name, shape, dtype, dev):
-    """A contiguous tensor, or None where the caller allows that."""
+    """Address of a contiguous tensor, or None for None where the caller allows that."""
     if t is None:
-        return
-    why = _bad(t, name, shape, dtype, dev)
-    if why is None and not t.is_contiguous():
-        why = "%s must be contiguous" % name
-    if why is not None:
-        raise ValueError(why)
+        return None
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == dev
+            and t.is_contiguous()):
+        _refuse(t, name, shape, dtype, dev, "%s must be contiguous" % name)
+    return t.data_ptr()
 
 
 def _rows(t, name, shape, dtype, dev):
     """The pitch of a row tensor [.., C]: elements from one row to the next, over all its rows."""
-    why = _bad(t, name, shape, dtype, dev)
-    if why is not None:
-        raise ValueError(why)
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == dev):
+        _refuse(t, name, shape, dtype, dev, None)
     if t.is_contiguous():
         return shape[-1]
     strides = t.stride()
@@ -91,8 +92,7 @@ def _call(name, dev, *args):
     if dev.type != "cuda":
         raise ValueError("%s needs tensors on a GPU, got %s" % (name, dev))
     fn = getattr(_lib.load(), name)
-    # the current stream's handle without a Stream object around it: 0.1 us against 1.9 us, of the
-    # 7 us that a single-token call takes on the host
+    # the current stream's handle without a Stream object around it: 0.1 us against 1.9 us
     if torch.cuda.current_device() == dev.index:
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
@@ -168,14 +168,13 @@ def _conv_fwd(x, w, bias, init, silu, want_last, cu=None, cu_host=None):
         raise ValueError("w must be a [D, W] tensor")
     W = w.shape[1]
     pitch = _rows(x, "x", x.shape, dt, dev)
-    _need(w, "w", (D, W), F32, dev)
-    _need(bias, "bias", (D,), F32, dev)
+    wp, bp = _need(w, "w", (D, W), F32, dev), _need(bias, "bias", (D,), F32, dev)
     edge = (seqs.n, max(W - 1, 0), D)
-    _need(init, "init", edge, dt, dev)
+    ip = _need(init, "init", edge, dt, dev)
     y = _like(x)
     last = torch.empty(edge, dtype=dt, device=dev) if want_last else None
-    _call(seqs.name("causal_conv_fwd"), dev, _ptr(x), pitch, _ptr(w), _ptr(bias), *seqs.offsets(),
-          _ptr(init), _ptr(y), _ptr(last), *seqs.sizes(x), D, W, int(bool(silu)), code)
+    _call(seqs.name("causal_conv_fwd"), dev, x.data_ptr(), pitch, wp, bp, *seqs.offsets(),
+          ip, y.data_ptr(), _ptr(last), *seqs.sizes(x), D, W, 1 if silu else 0, code)
     return {"y": y, "final": last} if want_last else {"y": y}
 
 
@@ -218,7 +217,7 @@ def _conv_bwd(dy, x, w, bias, init, dfinal, silu, cu=None, cu_host=None):
     ws = _workspace(n, dev)
     _call(seqs.name("causal_conv_bwd"), dev, _ptr(dy), dy_pitch, _ptr(x), pitch, _ptr(w), _ptr(bias),
           *seqs.offsets(), _ptr(init), _ptr(dfinal), _ptr(out["dx"]), _ptr(out.get("dinit")),
-          _ptr(out["dw"]), _ptr(out.get("dbias")), *seqs.sizes(x), D, W, int(bool(silu)), code,
+          _ptr(out["dw"]), _ptr(out.get("dbias")), *seqs.sizes(x), D, W, 1 if silu else 0, code,
           _ptr(ws), n)
     return out
 
@@ -236,9 +235,10 @@ def causal_conv_bwd_varlen(dy, x, w, cu_seqlens, bias=None, init=None, dfinal=No
 
 
 def _slots(state, slots, B, dev):
-    _need(slots, "slots", (B,), torch.int32, dev)
+    """Address of the slots."""
     if slots is None and state.shape[0] < B:
         raise ValueError("without slots the cache needs a slot a row: %d rows, %d slots" % (B, state.shape[0]))
+    return _need(slots, "slots", (B,), torch.int32, dev)
 
 
 def causal_conv_step(x, w, state, bias=None, *, slots=None, silu=True):
@@ -253,13 +253,12 @@ def causal_conv_step(x, w, state, bias=None, *, slots=None, silu=True):
         raise ValueError("w must be a [D, W] and state a [S, W-1, D] tensor")
     W, S = w.shape[1], state.shape[0]
     pitch = _rows(x, "x", x.shape, dt, dev)
-    _need(w, "w", (D, W), F32, dev)
-    _need(bias, "bias", (D,), F32, dev)
-    _need(state, "state", (S, max(W - 1, 0), D), dt, dev)
-    _slots(state, slots, B, dev)
+    wp, bp = _need(w, "w", (D, W), F32, dev), _need(bias, "bias", (D,), F32, dev)
+    sp = _need(state, "state", (S, max(W - 1, 0), D), dt, dev)
+    lp = _slots(state, slots, B, dev)
     y = _like(x)
-    _call("causal_conv_step", dev, _ptr(x), pitch, _ptr(w), _ptr(bias), _ptr(state), _ptr(slots), _ptr(y), B, S,
-          D, W, int(bool(silu)), code)
+    _call("causal_conv_step", dev, x.data_ptr(), pitch, wp, bp, sp, lp, y.data_ptr(), B, S, D, W, 1 if silu else 0,
+          code)
     return y
 
 
@@ -271,14 +270,13 @@ def _scan_args(x, dt_, A, Bm, Cm, skip, z, dt_bias, dev, dt):
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be a [D, N] tensor")
     N = A.shape[1]
-    px, pd = _rows(x, "x", x.shape, dt, dev), _rows(dt_, "dt", x.shape, dt, dev)
-    _need(A, "A", (D, N), F32, dev)
-    pb, pc = _rows(Bm, "Bm", (*lead, N), dt, dev), _rows(Cm, "Cm", (*lead, N), dt, dev)
-    _need(skip, "D", (D,), F32, dev)
-    _need(dt_bias, "dt_bias", (D,), F32, dev)
-    pz = _rows(z, "z", x.shape, dt, dev) if z is not None else 0
-    return N, (_ptr(x), px, _ptr(dt_), pd, _ptr(A), _ptr(Bm), pb, _ptr(Cm), pc), (_ptr(skip), _ptr(z), pz,
-                                                                                  _ptr(dt_bias))
+    shape, per_n = x.shape, (*lead, N)
+    px, pd = _rows(x, "x", shape, dt, dev), _rows(dt_, "dt", shape, dt, dev)
+    ap = _need(A, "A", (D, N), F32, dev)
+    pb, pc = _rows(Bm, "Bm", per_n, dt, dev), _rows(Cm, "Cm", per_n, dt, dev)
+    kp, tp = _need(skip, "D", (D,), F32, dev), _need(dt_bias, "dt_bias", (D,), F32, dev)
+    zp, pz = (z.data_ptr(), _rows(z, "z", shape, dt, dev)) if z is not None else (None, 0)
+    return N, (x.data_ptr(), px, dt_.data_ptr(), pd, ap, Bm.data_ptr(), pb, Cm.data_ptr(), pc), (kp, zp, pz, tp)
 
 
 def _scan_workspace(which, seqs, x, N):
@@ -300,7 +298,7 @@ def _scan_fwd(x, dt, A, Bm, Cm, skip, z, dt_bias, h0, softplus, want_ht, want_h,
     n = _scan_workspace("fwd", seqs, x, N)
     ws = _workspace(n, dev)
     _call(seqs.name("ssm_scan_fwd"), dev, *ins, *seqs.offsets(), *opts, _ptr(h0), _ptr(y), _ptr(ht), _ptr(h),
-          *seqs.sizes(x), D, N, int(bool(softplus)), code, _ptr(ws), n)
+          *seqs.sizes(x), D, N, 1 if softplus else 0, code, _ptr(ws), n)
     out = {"y": y}
     if want_ht:
         out["ht"] = ht
@@ -356,7 +354,7 @@ def _scan_bwd(dy, h, x, dt, A, Bm, Cm, skip, z, dt_bias, dht, softplus, want_dh0
     g = out.get
     _call(seqs.name("ssm_scan_bwd"), dev, _ptr(dy), dy_pitch, _ptr(h), *ins, *seqs.offsets(), *opts, _ptr(dht),
           _ptr(g("dx")), _ptr(g("ddt")), _ptr(g("dA")), _ptr(g("dB")), _ptr(g("dC")), _ptr(g("dD")),
-          _ptr(g("dz")), _ptr(g("ddt_bias")), _ptr(g("dh0")), *seqs.sizes(x), D, N, int(bool(softplus)), code,
+          _ptr(g("dz")), _ptr(g("ddt_bias")), _ptr(g("dh0")), *seqs.sizes(x), D, N, 1 if softplus else 0, code,
           _ptr(ws), n)
     return out
 
@@ -386,10 +384,10 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, slots=Non
         raise ValueError("state must be a [S, C, N] tensor")
     N, ins, opts = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, dev, ty)
     S = state.shape[0]
-    _need(state, "state", (S, C, N), F32, dev)
-    _slots(state, slots, B, dev)
+    sp = _need(state, "state", (S, C, N), F32, dev)
+    lp = _slots(state, slots, B, dev)
     y = _like(x)
-    _call("ssm_step", dev, *ins, *opts, _ptr(state), _ptr(slots), _ptr(y), B, S, C, N, int(bool(softplus)), code)
+    _call("ssm_step", dev, *ins, *opts, sp, lp, y.data_ptr(), B, S, C, N, 1 if softplus else 0, code)
     return y
 
 
@@ -399,16 +397,17 @@ def _norm_args(x, w, residual):
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise ValueError("x must be a tensor [.., D]")
     dev, dt, code = _act(x, "x", x.dim())
-    D = x.shape[-1]
-    pitch = _rows(x, "x", x.shape, dt, dev)
-    _need(w, "w", (D,), F32, dev)
-    rcode, rpitch = code, 0
+    shape = x.shape
+    D = shape[-1]
+    pitch = _rows(x, "x", shape, dt, dev)
+    wp = _need(w, "w", (D,), F32, dev)
+    rcode, rpitch, rp = code, 0, None
     if residual is not None:
         if not isinstance(residual, torch.Tensor) or residual.dtype not in _DT:
             raise ValueError("residual must be a float32 or bfloat16 tensor")
         rcode = _DT[residual.dtype]
-        rpitch = _rows(residual, "residual", x.shape, residual.dtype, dev)
-    return dev, dt, code, rcode, D, x.numel() // max(D, 1), pitch, rpitch
+        rp, rpitch = residual.data_ptr(), _rows(residual, "residual", shape, residual.dtype, dev)
+    return dev, code, rcode, D, x.numel() // max(D, 1), (x.data_ptr(), pitch, rp, rpitch, wp)
 
 
 def rms_norm_fwd(x, w, residual=None, eps=1e-5, *, want_rstd=False):
@@ -417,14 +416,17 @@ def rms_norm_fwd(x, w, residual=None, eps=1e-5, *, want_rstd=False):
 
     x [..,D] (fp32 or bf16; rows may be pitched), w [D] fp32, residual [..,D] of x's type or fp32.
     Returns y, sum where a residual is given, and rstd [..] fp32 (for rms_norm_bwd) when requested."""
-    dev, dt, code, rcode, D, M, pitch, rpitch = _norm_args(x, w, residual)
-    out = {"y": _like(x)}
+    dev, code, rcode, D, M, ins = _norm_args(x, w, residual)
+    y = _like(x)
+    out = {"y": y}
+    sp = rp = None
     if residual is not None:
-        out["sum"] = _like(residual)
+        out["sum"] = s = _like(residual)
+        sp = s.data_ptr()
     if want_rstd:
-        out["rstd"] = torch.empty(x.shape[:-1], dtype=F32, device=dev)
-    _call("rms_norm_fwd", dev, _ptr(x), pitch, _ptr(residual), rpitch, _ptr(w), float(eps), _ptr(out["y"]),
-          _ptr(out.get("sum")), _ptr(out.get("rstd")), M, D, code, rcode)
+        out["rstd"] = r = torch.empty(x.shape[:-1], dtype=F32, device=dev)
+        rp = r.data_ptr()
+    _call("rms_norm_fwd", dev, *ins, eps, y.data_ptr(), sp, rp, M, D, code, rcode)
     return out
 
 
@@ -434,13 +436,13 @@ def rms_norm_q8_fwd(x, w, residual=None, eps=1e-5, *, block=0):
     block 0: one scale a row, scale [..,1]; block 128: one for each 128 columns, scale
     [..,ceil(D/128)].  ``scale = max(max |y|, 1e-12) / 448``.  Returns q, scale, and sum where a
     residual is given."""
-    dev, dt, code, rcode, D, M, pitch, rpitch = _norm_args(x, w, residual)
+    dev, code, rcode, D, M, ins = _norm_args(x, w, residual)
     out = {"q": torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=dev),
            "scale": torch.empty(*x.shape[:-1], (D + 127) // 128 if block else 1, dtype=F32, device=dev)}
     if residual is not None:
         out["sum"] = _like(residual)
-    _call("rms_norm_q8_fwd", dev, _ptr(x), pitch, _ptr(residual), rpitch, _ptr(w), float(eps), int(block),
-          _ptr(out["q"]), _ptr(out["scale"]), _ptr(out.get("sum")), M, D, code, rcode)
+    _call("rms_norm_q8_fwd", dev, *ins, eps, int(block), _ptr(out["q"]), _ptr(out["scale"]), _ptr(out.get("sum")),
+          M, D, code, rcode)
     return out
 
 
