@@ -74,6 +74,10 @@ hipError_t launch_conv_step(const ConvStepParams& p, int dtype, hipStream_t st);
 constexpr int kSsmChunk = 16;
 constexpr int kSsmBlock = 32;
 constexpr int kSsmMaxN = 64;
+inline int ssm_channels(int N) { return N <= 16 ? 64 : 16; }  // of a workgroup
+
+// Workgroups of 256 threads that a launch can have: it takes fewer than 2^32 threads.
+constexpr int64_t kMaxGroups = (1 << 24) - 1;
 
 // How long sequences are cut: segments of `seg` tokens (a multiple of kSsmBlock), nseg in all, are
 // summarised and joined; the pass proper takes `main` tokens (a multiple of seg) at a time, nmain in all.

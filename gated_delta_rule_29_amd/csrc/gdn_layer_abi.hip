@@ -73,18 +73,22 @@ int check_conv(const void* x, int64_t pitch, const float* w, int D, int W, int d
   return check_pitch("x", x, pitch, D);
 }
 
-// Workgroups of 256 threads, one thread a channel in the smallest instance: `per` of them a row.
-int check_grid(int64_t rows, int64_t per, const char* what) {
-  if (rows * per > INT32_MAX)
+int check_grid(int64_t groups, const char* what) {
+  if (groups > gdn::kMaxGroups)
     return fail(GDN_ERR_INVALID, "%s of these sizes exceeds the grid limit", what);
   return GDN_OK;
+}
+
+// One thread a channel and 32 tokens in the smallest instance (fewer tokens in small calls only).
+int check_conv_grid(const gdn::Seqs& s, int D, const char* what) {
+  return check_grid(((int64_t)((s.rows + 31) / 32) * D + 255) / 256, what);
 }
 
 int conv_fwd(const gdn::Seqs& s, const void* x, int64_t x_pitch, const float* w, const float* bias,
              const void* init, void* y, void* last, int D, int W, int silu, int dtype, void* stream) {
   GDN_TRY(check_conv(x, x_pitch, w, D, W, dtype));
   if (!y) return fail(GDN_ERR_INVALID, "y must be a non-null device pointer");
-  GDN_TRY(check_grid(s.rows, (D + 255) / 256, "causal_conv_fwd"));
+  GDN_TRY(check_conv_grid(s, D, "causal_conv_fwd"));
   const gdn::ConvParams p{x, x_pitch, w, bias, init, y, last, s, D, W, silu != 0};
   const hipError_t e = gdn::launch_conv_fwd(p, dtype, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "causal_conv_fwd launch");
@@ -97,7 +101,7 @@ int conv_bwd(const gdn::Seqs& s, const void* dy, int64_t dy_pitch, const void* x
   GDN_TRY(check_conv(x, x_pitch, w, D, W, dtype));
   if (!dy || !dx || !dw) return fail(GDN_ERR_INVALID, "dy, dx and dw must be non-null device pointers");
   GDN_TRY(check_pitch("dy", dy, dy_pitch, D));
-  GDN_TRY(check_grid(s.rows, (D + 255) / 256, "causal_conv_bwd"));
+  GDN_TRY(check_conv_grid(s, D, "causal_conv_bwd"));
   GDN_TRY(check_workspace(ws, ws_bytes, gdn::conv_bwd_ws_bytes(s.rows, D, W)));
   gdn::ConvBwdParams p{};
   p.f = gdn::ConvParams{x, x_pitch, w, bias, init, nullptr, nullptr, s, D, W, silu != 0};
@@ -154,10 +158,10 @@ gdn::SsmParams scan_params(const gdn::Seqs& s, const Split& sp, const int* cu_ho
   return p;
 }
 
-// One workgroup a segment and 16 channels in the smallest instance; 256 states in the joins.
-int check_scan_grid(const gdn::Seqs& s, const Split& sp, int D, int N) {
-  GDN_TRY(check_grid(sp.nseg, (D + 15) / 16, "ssm_scan"));
-  return check_grid(s.n, ((int64_t)D * N + 255) / 256, "ssm_scan");
+// (The joins, of 256 states a workgroup, run where sequences times channels are few.)
+int check_scan_grid(const Split& sp, int D, int N) {
+  const int ch = gdn::ssm_channels(N);
+  return check_grid((int64_t)sp.nseg * ((D + ch - 1) / ch), "ssm_scan");
 }
 
 int scan_fwd(const gdn::Seqs& s, const Split& sp, const int* cu_host, const Scan& a, const float* h0, void* y, float* ht,
@@ -166,7 +170,7 @@ int scan_fwd(const gdn::Seqs& s, const Split& sp, const int* cu_host, const Scan
   GDN_TRY(check_state("h0", h0, N));
   GDN_TRY(check_state("ht", ht, N));
   GDN_TRY(check_state("h", h, N));
-  GDN_TRY(check_scan_grid(s, sp, D, N));
+  GDN_TRY(check_scan_grid(sp, D, N));
   GDN_TRY(check_workspace(ws, ws_bytes, gdn::ssm_fwd_ws_bytes(sp, s.n, D, N)));
   gdn::SsmParams p = scan_params(s, sp, cu_host, a, D, N, softplus);
   p.h0 = h0; p.y = y; p.ht = ht; p.h = h;
@@ -190,8 +194,7 @@ int scan_bwd(const gdn::Seqs& s, const Split& sp, const int* cu_host, const Scan
   GDN_TRY(check_state("h", h, N));
   GDN_TRY(check_state("dht", dht, N));
   GDN_TRY(check_state("dh0", o.dh0, N));
-  GDN_TRY(check_scan_grid(s, sp, D, N));
-  GDN_TRY(check_grid(s.rows, (2 * N + 63) / 64, "ssm_scan_bwd"));
+  GDN_TRY(check_scan_grid(sp, D, N));
   GDN_TRY(check_workspace(ws, ws_bytes, gdn::ssm_bwd_ws_bytes(sp, s.rows, D, N)));
   gdn::SsmBwdParams p{};
   p.f = scan_params(s, sp, cu_host, a, D, N, softplus);
@@ -203,10 +206,11 @@ int scan_bwd(const gdn::Seqs& s, const Split& sp, const int* cu_host, const Scan
   return e == hipSuccess ? ok() : hip_fail(e, "ssm_scan_bwd launch");
 }
 
-int check_step(int B, int S, const int* slots, int D) {
+// ch: channels of a workgroup in a large call's smallest instance.
+int check_step(int B, int S, const int* slots, int D, int ch) {
   if (B <= 0 || S <= 0) return fail(GDN_ERR_INVALID, "B and S must be positive (got %d, %d)", B, S);
   if (!slots && S < B) return fail(GDN_ERR_INVALID, "without slots the cache needs a slot a row (S = %d, B = %d)", S, B);
-  return check_grid(B, (D + 15) / 16, "a step");
+  return check_grid((int64_t)B * ((D + ch - 1) / ch), "a step");
 }
 
 // -------------------------------------------------------------------------------------- norm
@@ -283,7 +287,7 @@ int causal_conv_step(const void* x, int64_t x_pitch, const float* w, const float
                      void* y, int B, int S, int D, int W, int silu, int dtype, void* stream) {
   GDN_TRY(check_conv(x, x_pitch, w, D, W, dtype));
   if (!state || !y) return fail(GDN_ERR_INVALID, "state and y must be non-null device pointers");
-  GDN_TRY(check_step(B, S, slots, D));
+  GDN_TRY(check_step(B, S, slots, D, 256));
   const gdn::ConvStepParams p{x, x_pitch, w, bias, state, slots, y, B, S, D, W, silu != 0};
   const hipError_t e = gdn::launch_conv_step(p, dtype, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ok() : hip_fail(e, "causal_conv_step launch");
@@ -381,7 +385,7 @@ int ssm_step(const void* x, int64_t x_pitch, const void* dt, int64_t dt_pitch, c
   GDN_TRY(check_scan(a, D, N, dtype));
   if (!state || !y) return fail(GDN_ERR_INVALID, "state and y must be non-null device pointers");
   GDN_TRY(check_state("state", state, N));
-  GDN_TRY(check_step(B, S, slots, D));
+  GDN_TRY(check_step(B, S, slots, D, 4 * gdn::ssm_channels(N)));
   const gdn::SsmStepParams p{x, dt, z, Bm, Cm, x_pitch, dt_pitch, z_pitch, b_pitch, c_pitch, A, skip, dt_bias,
                              state, slots, y, B, S, D, N, softplus != 0};
   const hipError_t e = gdn::launch_ssm_step(p, dtype, static_cast<hipStream_t>(stream));

@@ -157,10 +157,11 @@ __device__ __forceinline__ float wave_sum(float x) {
 // out(c, sum over r < rows of part[r][c]) for every column c < cols: 64 columns a workgroup, 16
 // waves that each take every 16th row, joined in a fixed order.
 template <typename Out>
-__global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ part, int rows, int64_t cols, Out out) {
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ part, int rows, int64_t cols,
+                                                          int64_t first, Out out) {
   __shared__ float acc[16][64];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t c = first + (int64_t)blockIdx.x * 64 + lane;
   float s = 0.f;
   if (c < cols) {
 #pragma unroll 4
@@ -177,8 +178,15 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 }
 template <typename Out>
 hipError_t column_sum(const float* part, int rows, int64_t cols, Out out, hipStream_t st) {
-  column_sum_kernel<<<dim3((unsigned)((cols + 63) / 64)), 1024, 0, st>>>(part, rows, cols, out);
-  return hipGetLastError();
+  // (a launch takes fewer than 2^32 threads, 16 a column)
+  constexpr int64_t most = int64_t{1} << 27;
+  for (int64_t first = 0; first < cols; first += most) {
+    const int64_t n = cols - first < most ? cols - first : most;
+    column_sum_kernel<<<dim3((unsigned)((n + 63) / 64)), 1024, 0, st>>>(part, rows, cols, first, out);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Whether a row before row b uses the same slot: the first row of a slot is the one that counts.

@@ -323,6 +323,24 @@ hipError_t by_type(int dtype, int rdtype, F&& f) {
   return rdtype == GDN_DTYPE_BF16 ? f(bf16{}, bf16{}) : f(bf16{}, float{});
 }
 
+// The call for M of the rows, from row m0 on.
+template <typename T, typename RT>
+NormParams rows_from(NormParams p, int m0, int M) {
+  const int64_t out = (int64_t)m0 * p.D;
+  p.x = static_cast<const T*>(p.x) + m0 * p.x_pitch;
+  if (p.residual) p.residual = static_cast<const RT*>(p.residual) + m0 * p.r_pitch;
+  if (p.sum) p.sum = static_cast<RT*>(p.sum) + out;
+  if (p.rstd) p.rstd += m0;
+  if (p.scale) {
+    p.y = static_cast<uint8_t*>(p.y) + out;
+    p.scale += m0 * (int64_t)(p.block ? (p.D + kBlock - 1) / kBlock : 1);
+  } else {
+    p.y = static_cast<T*>(p.y) + out;
+  }
+  p.M = M;
+  return p;
+}
+
 // Row workers of a gradient call: four workgroups a CU at most.
 int bwd_groups(int M, int D) {
   const int most = D <= 512 ? 4096 : 1024;
@@ -342,11 +360,18 @@ hipError_t launch_norm_fwd(const NormParams& p, int dtype, int rdtype, hipStream
       constexpr int TPR = decltype(tpr)::value, wg = TPR < 256 ? 256 : TPR, rpw = wg / TPR;
       using T = decltype(t);
       using RT = decltype(rt);
-      const dim3 grid((p.M + rpw - 1) / rpw);
-      if (!q8) norm_fwd_kernel<T, RT, v(), TPR, nv(), 0><<<grid, wg, 0, st>>>(p);
-      else if (p.block == 0) norm_fwd_kernel<T, RT, v(), TPR, nv(), 1><<<grid, wg, 0, st>>>(p);
-      else norm_fwd_kernel<T, RT, v(), TPR, nv(), 2><<<grid, wg, 0, st>>>(p);
-      return hipGetLastError();
+      // A launch takes fewer than 2^32 threads, which a few million rows reach: more rows, more launches.
+      constexpr int most = (1 << 30) / wg * rpw;
+      for (int m0 = 0; m0 < p.M; m0 += most) {
+        const NormParams q = rows_from<T, RT>(p, m0, min(p.M - m0, most));
+        const dim3 grid((q.M + rpw - 1) / rpw);
+        if (!q8) norm_fwd_kernel<T, RT, v(), TPR, nv(), 0><<<grid, wg, 0, st>>>(q);
+        else if (p.block == 0) norm_fwd_kernel<T, RT, v(), TPR, nv(), 1><<<grid, wg, 0, st>>>(q);
+        else norm_fwd_kernel<T, RT, v(), TPR, nv(), 2><<<grid, wg, 0, st>>>(q);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+      }
+      return hipSuccess;
     });
   });
 }

@@ -234,7 +234,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmStepParams p, int grou
 // The gradient's registers allow two waves a SIMD and no more, so that it takes pieces of several
 // segments, and only what is behind the first piece has to be summarised.
 SsmSplit ssm_split(bool backward, const int* cu, int n, int T, int D, int N) {
-  const int ch = N <= 16 ? 16 : 4;  // channels of a wave
+  const int ch = ssm_channels(N) / 4;  // channels of a wave
   const int64_t per_seg = (D + ch - 1) / ch;
   int longest = cu ? 1 : T;
   for (int i = 0; cu && i < n; ++i) longest = cu[i + 1] - cu[i] > longest ? cu[i + 1] - cu[i] : longest;

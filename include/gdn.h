@@ -635,8 +635,9 @@ GDN_API int gdn_bwd_dhu_varlen(const void* q, const void* k, const void* w, cons
  *  - x [tokens, C] with a pitch: row r starts at x + r * pitch elements.  A dense batch of B
  *    sequences of T tokens has rows b * T + t; a packed batch (_varlen) has T_total rows,
  *    sequence i covering rows [cu[i], cu[i+1]), with cu_seqlens and cu_seqlens_host as in
- *    gdn_fwd_varlen.  Outputs are dense.  A call has at most GDN_MAX_TOKENS rows
- *    (GDN_ERR_INVALID); pitches beyond GDN_MAX_PITCH are
+ *    gdn_fwd_varlen.  Outputs are dense.  A call has at most GDN_MAX_TOKENS rows, and a
+ *    scan or step fewer than 2^24 workgroups (of 64 channels of a sequence where N <= 16, of 16
+ *    beyond; of 256 in a convolution's step): GDN_ERR_INVALID; pitches beyond GDN_MAX_PITCH are
  *    GDN_ERR_UNSUPPORTED (32 rows are addressed with 32-bit offsets).
  *  - dtype is that of the activations (inputs and outputs that are not said to be fp32);
  *    all arithmetic, states and sums over tokens or channels are fp32, each result rounded once.

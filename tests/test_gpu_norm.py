@@ -121,3 +121,21 @@ def test_gradient_over_many_rows_is_deterministic():
     check("dw", a["dw"], ref["dw"])
     check("dx", a["dx"], ref["ds"])
     assert torch.equal(a["dw"], b["dw"])
+
+
+@pytest.mark.parametrize("D,seam", [(513, 1 << 20), (8, 1 << 24)])
+def test_more_rows_than_one_launch_takes(D, seam):
+    """The rows around the seam between two launches are those of a call on them alone, bit for bit."""
+    import gated_delta_rule_29_amd as g
+
+    say("norm rows around %d, D %d" % (seam, D))
+    M, part = seam + 5, slice(seam - 3, seam + 5)
+    x = torch.randn(M, D, device=DEV, dtype=torch.bfloat16)
+    w = torch.rand(D, device=DEV) + 0.5
+    for call, kw in ((g.rms_norm_fwd, dict(want_rstd=True)), (g.rms_norm_q8_fwd, {}), (g.rms_norm_q8_fwd, dict(block=128))):
+        full, alone = call(x, w, residual=x, **kw), call(x[part], w, residual=x[part], **kw)
+        for k in alone:
+            a, b = full[k][part], alone[k]
+            if k == "q":
+                a, b = a.view(torch.uint8), b.view(torch.uint8)
+            assert torch.equal(a, b), (call.__name__, k)

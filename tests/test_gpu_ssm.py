@@ -288,3 +288,22 @@ def test_states_that_last(varied, inputs, bound):
     err = float(((state.cpu().double() - ref[None]).abs() / ref).max()) * 2 ** 24
     say("  error %.1f u" % err)
     assert err <= bound
+
+
+def test_more_rows_than_one_sum_takes():
+    """dB and dC of 2^20 rows of 64 states are 2^27 sums, which one launch takes; the sequences around
+    that row are those of a call on them alone, bit for bit (neither call is cut)."""
+    import gated_delta_rule_29_amd as g
+
+    n, T, D, N = 8200, 128, 2, 64
+    say("scan gradient of %d rows" % (n * T))
+    r = lambda *s: torch.randn(*s, device=DEV)
+    a = dict(x=r(n, T, D), dt=r(n, T, D), Bm=r(n, T, N), Cm=r(n, T, N))
+    A, dy, part = -torch.rand(D, N, device=DEV) - 0.1, r(n, T, D), slice(8190, 8200)
+    def run(s):
+        c = {k: v[s] for k, v in a.items()}
+        f = g.ssm_scan_fwd(c["x"], c["dt"], A, c["Bm"], c["Cm"], want_h=True)
+        return g.ssm_scan_bwd(dy[s], f["h"], c["x"], c["dt"], A, c["Bm"], c["Cm"])
+    full, alone = run(slice(0, n)), run(part)
+    for k in ("dx", "ddt", "dB", "dC"):
+        assert torch.equal(full[k][part], alone[k]), k

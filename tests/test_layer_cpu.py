@@ -73,13 +73,14 @@ def test_conv_codes():
     for bad in (dict(st=None), dict(y=None), dict(B=0), dict(S=0), dict(S=1)):
         assert step(**bad) == L.ERR_INVALID, bad
     assert step(W=7) == L.ERR_UNSUPPORTED
+    assert step(B=1 << 24, S=1 << 24) == L.ERR_INVALID  # a workgroup a row: 2^32 threads
 
 
 def _scan(lib, **kw):
-    a = dict(x=FAKE, xp=8, dt=FAKE, A=FAKE, B_=FAKE, bp=16, C_=FAKE, z=None, zp=0, h0=None, y=FAKE, ht=None, h=None,
+    a = dict(x=FAKE, xp=8, dt=FAKE, dp=8, A=FAKE, B_=FAKE, bp=16, C_=FAKE, z=None, zp=0, h0=None, y=FAKE, ht=None, h=None,
              B=1, T=4, D=8, N=16, ty=1, ws=None, n=0)
     a.update(kw)
-    return lib.ssm_scan_fwd(a["x"], a["xp"], a["dt"], 8, a["A"], a["B_"], a["bp"], a["C_"], 64, None, a["z"],
+    return lib.ssm_scan_fwd(a["x"], a["xp"], a["dt"], a["dp"], a["A"], a["B_"], a["bp"], a["C_"], 64, None, a["z"],
                             a["zp"], None, a["h0"], a["y"], a["ht"], a["h"], a["B"], a["T"], a["D"], a["N"], 1,
                             a["ty"], a["ws"], a["n"], None)
 
@@ -88,7 +89,8 @@ def test_scan_codes():
     L, lib = _lib()
     for bad in (dict(x=None), dict(dt=None), dict(A=None), dict(B_=None), dict(C_=None), dict(y=None), dict(B=0),
                 dict(T=0), dict(D=0), dict(N=0), dict(ty=3), dict(xp=7), dict(bp=15), dict(z=FAKE, zp=7),
-                dict(A=ODD), dict(h0=ODD), dict(ht=ODD), dict(h=ODD), dict(B=1 << 16, T=1 << 16)):
+                dict(A=ODD), dict(h0=ODD), dict(ht=ODD), dict(h=ODD), dict(B=1 << 16, T=1 << 16),
+                dict(B=1 << 18, T=1, D=1 << 12, xp=1 << 12, dp=1 << 12)):  # (2^24 workgroups: 2^32 threads)
         assert _scan(lib, **bad) == L.ERR_INVALID, bad
     assert _scan(lib, N=65, bp=65) == L.ERR_UNSUPPORTED
     # a long sequence of few channels is cut and needs a workspace; a short or a wide one does not
@@ -136,7 +138,7 @@ def test_step_and_norm_codes():
         return lib.ssm_step(FAKE, 8, FAKE, 8, FAKE, FAKE, 64, FAKE, 64, None, None, 0, None, a["st"], None, a["y"],
                             a["B"], a["S"], 8, a["N"], 1, 1, None)
 
-    for bad in (dict(st=None), dict(st=ODD), dict(y=None), dict(B=0), dict(S=1)):
+    for bad in (dict(st=None), dict(st=ODD), dict(y=None), dict(B=0), dict(S=1), dict(B=1 << 24, S=1 << 24)):
         assert step(**bad) == L.ERR_INVALID, bad
     assert step(N=65) in (L.ERR_INVALID, L.ERR_UNSUPPORTED)
 
