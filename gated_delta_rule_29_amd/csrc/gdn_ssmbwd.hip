@@ -162,8 +162,8 @@ __global__ __launch_bounds__(256) void ssm_bwd_summary_kernel(SsmBwdParams p, in
   if (w.cv && j == 0) f.seg_sum[(int64_t)w.seg * f.D + w.c] = dsum;
 }
 
-// A sequence's segments from the last to the last one of its first piece: seg_state becomes the
-// gradient that reaches each segment's last state from behind it.
+// A sequence's segments from the last to the last one of its first piece (of its only one where it is
+// shorter than a piece): seg_state becomes the gradient that reaches each segment's last state from behind it.
 __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(SsmBwdParams p, int per_seq) {
   const SsmParams& f = p.f;
   const int seq = blockIdx.x / per_seq;
@@ -174,8 +174,8 @@ __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(SsmBwdParams p, int p
   const int64_t d = e / f.N;
   const float a = f.A[e] * kLog2e;
   float g = p.dht ? p.dht[seq * DN + e] : 0.f;
-  const int first = f.split.main / f.split.seg;
-  for (int i = sp.count - 1; i >= first - 1 && i >= 0; --i) {
+  const int first = f.split.main / f.split.seg, stop = min(first, sp.count) - 1;
+  for (int i = sp.count - 1; i >= stop && i >= 0; --i) {
     const int64_t s = sp.first + i;
     const bool summed = i >= first;
     const float own = summed ? f.seg_state[s * DN + e] : 0.f, sum = summed ? f.seg_sum[s * f.D + d] : 0.f;

@@ -307,3 +307,56 @@ def test_more_rows_than_one_sum_takes():
     full, alone = run(slice(0, n)), run(part)
     for k in ("dx", "ddt", "dB", "dC"):
         assert torch.equal(full[k][part], alone[k]), k
+
+
+def _pieces(lib, cu_host, rows, D, N):
+    """(segments, pieces) of a packed gradient, from the workspaces' sizes."""
+    n, al = cu_host.numel() - 1, lambda b: -(-b // 256) * 256  # noqa: E731
+    nseg = lib.ssm_scan_fwd_varlen_workspace_bytes(cu_host.data_ptr(), n, D, N) // (D * (N + 1) * 4)
+    groups = -(-D // (64 if N <= 16 else 16))
+    left = lib.ssm_scan_bwd_varlen_workspace_bytes(cu_host.data_ptr(), n, D, N)
+    left -= al(nseg * D * N * 4) + al(nseg * D * 4) + al(groups * rows * 2 * N * 4)
+    return nseg, left // (D * (N + 2) * 4)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("full", [True, False])
+@pytest.mark.parametrize("lens,D,N", [([40, 1500, 1, 600, 3], 1024, 16), ([2048, 100], 2048, 16),
+                                      ([1, 333, 77, 33, 190], 1000, 24), ([1200, 20, 1280], 300, 40)])
+def test_packed_gradient_of_short_sequences_beside_cut_ones(lens, D, N, full, dtype):
+    """Packed gradients whose pieces have several segments, with sequences shorter than a piece first, between
+    and last, on a workspace full of NaN: what a sequence starts from is written by the call.
+
+    Tolerance: that of test_cut_gradient_agrees_with_pieces for one result (40 roundings, and 0.6 sqrt(M) +
+    0.03 M of a state that lasts M tokens, here as long as the longest sequence), and 0.6 sqrt(M) for a sum
+    over M tokens in one register; of the largest element."""
+    from gated_delta_rule_29_amd import _lib
+
+    import gated_delta_rule_29_amd as g
+
+    say("packed gradient %s D %d N %d full %s %s" % (lens, D, N, full, dtype))
+    lib, T, n, M = _lib.load(), sum(lens), len(lens), max(lens)
+    c, d, cu_h = _inputs(lens, False, D, N, (0, 0), dtype, D + N)
+    nseg, nmain = _pieces(lib, cu_h, T, D, N)
+    assert nseg > nmain > n  # pieces of several segments, and some sequence in several pieces
+    cu, t = cu_h.to(DEV), TYPES[dtype]
+    opt = dict(D=d["skip"], z=d["z"], dt_bias=d["dt_bias"], h0=d["h0"]) if full else {}
+    h = g.ssm_scan_fwd_varlen(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], cu, want_h=True, cu_seqlens_host=cu_h, **opt)["h"]
+    p = lambda k: d[k].data_ptr() if full or k not in ("skip", "z", "dt_bias", "dht") else None  # noqa: E731
+    nan = lambda *s, ty=torch.float32: torch.full(s, float("nan"), dtype=ty, device=DEV)  # noqa: E731
+    o = dict(dx=nan(T, D, ty=t), ddt=nan(T, D, ty=t), dA=nan(D, N), dB=nan(T, N, ty=t), dC=nan(T, N, ty=t), dh0=nan(n, D, N))
+    if full:
+        o.update(dD=nan(D), dz=nan(T, D, ty=t), ddt_bias=nan(D))
+    q = lambda k: o[k].data_ptr() if k in o else None  # noqa: E731
+    size = lib.ssm_scan_bwd_varlen_workspace_bytes(cu_h.data_ptr(), n, D, N)
+    ws = nan(size // 4)
+    assert lib.ssm_scan_bwd_varlen(
+        p("dy"), D, h.data_ptr(), p("x"), D, p("dt"), D, p("A"), p("Bm"), N, p("Cm"), N, cu.data_ptr(), cu_h.data_ptr(), n,
+        p("skip"), p("z"), D, p("dt_bias"), p("dht"), q("dx"), q("ddt"), q("dA"), q("dB"), q("dC"), q("dD"), q("dz"),
+        q("ddt_bias"), q("dh0"), T, D, N, 1, 1 if dtype == "bf16" else 0, ws.data_ptr(), size,
+        torch.cuda.current_stream().cuda_stream) == 0, _lib.last_error()
+    torch.cuda.synchronize()
+    ref = L.scan_bwd(lens, flat(c["dy"]), dht=arr(c["dht"]) if full else None, **_ref(c, full))
+    u = 2.0 ** -24 * (40 + 1.2 * M ** 0.5 + 0.03 * M)
+    for k in o:
+        check(k, o[k], ref[k], u * float(np.abs(ref[k]).max() / np.sqrt((ref[k] * ref[k]).mean())))
