@@ -99,13 +99,15 @@ __device__ __forceinline__ float scale_of(unsigned amax) {
   return (a == a ? fmaxf(a, 1e-12f) : a) / kE4m3Max;
 }
 
-// e4m3 bytes of y / scale (to nearest even).  The quotient is at most 448 but for its last bit.
+// e4m3 bytes of y / scale (to nearest even).  The quotient is at most 448 but for its last bit.  It is
+// divided for: a product with the scale's reciprocal may be a unit or two away from it, on the other side
+// of a value half way between two e4m3 values.
 template <int V>
-__device__ __forceinline__ void store_q8(uint8_t* q, const float (&y)[V], float inv) {
+__device__ __forceinline__ void store_q8(uint8_t* q, const float (&y)[V], float scale) {
   float v[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    v[i] = y[i] * inv;
+    v[i] = y[i] / scale;
     v[i] = v[i] > kE4m3Max ? kE4m3Max : (v[i] < -kE4m3Max ? -kE4m3Max : v[i]);  // NaN passes
   }
   if constexpr (V == 8) {
@@ -181,7 +183,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormPar
         const float s = scale_of(max16(m));
         if (c < p.D) {
           if (tid % 16 == 0) p.scale[(int64_t)row * ((p.D + kBlock - 1) / kBlock) + c / kBlock] = s;
-          store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[i], 1.f / s);
+          store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[i], s);
         }
       } else if constexpr (TPR > 64) {
         m = wave_max(m);  // a wave holds half a block
@@ -192,11 +194,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormPar
   if constexpr (Q8 == 1) {
     const float s = scale_of(row_max<TPR>(amax, rd));
     if (tid == 0) p.scale[row] = s;
-    const float inv = 1.f / s;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + tid) * V;
-      if (c < p.D) store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[i], inv);
+      if (c < p.D) store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[i], s);
     }
   }
   if constexpr (Q8 == 2 && V == 1 && TPR == 64) {
@@ -210,7 +211,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormPar
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int c = (2 * b + h) * TPR + tid;
-        if (c < p.D) store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[2 * b + h], 1.f / s);
+        if (c < p.D) store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[2 * b + h], s);
       }
     }
   }
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormPar
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = i * TPR + tid;
-      if (c < p.D) store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[i], 1.f / scale(c / kBlock));
+      if (c < p.D) store_q8<V>(static_cast<uint8_t*>(p.y) + (int64_t)row * p.D + c, v[i], scale(c / kBlock));
     }
   }
 }

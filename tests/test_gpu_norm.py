@@ -139,3 +139,29 @@ def test_more_rows_than_one_launch_takes(D, seam):
             if k == "q":
                 a, b = a.view(torch.uint8), b.view(torch.uint8)
             assert torch.equal(a, b), (call.__name__, k)
+
+
+def _e4m3_midpoints():
+    """Every value half way between two neighbouring e4m3 values (0 .. 448)."""
+    v = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    return (v[1:] + v[:-1]) / 2
+
+
+@pytest.mark.parametrize("block", [0, 128])
+@pytest.mark.parametrize("D", [256, 250, 1030])  # 16-byte vectors, single columns in one wave and in many
+def test_eight_bits_round_the_quotient(D, block):
+    """Values whose quotient by the scale is half way between two e4m3 values, or next to it: q is e4m3 of the
+    fp32 quotient y / scale, bit for bit.  (Rows of ones with an eps that adds nothing: y is w.)"""
+    import gated_delta_rule_29_amd as g
+
+    say("norm q8 of midpoints D %d block %d" % (D, block))
+    mid, r = _e4m3_midpoints(), gen(D + block)
+    for _ in range(8):
+        largest = 1 + torch.rand(1, generator=r)
+        s = largest / 448  # fp32, as the scale is formed
+        w = (mid[torch.randint(mid.numel(), (D,), generator=r)] * s.double()).float()
+        w *= torch.randint(0, 2, (D,), generator=r) * 2 - 1
+        w[::128] = largest
+        o = g.rms_norm_q8_fwd(torch.ones(2, D, device=DEV), w.to(DEV), eps=1e-30, block=block)
+        assert (o["scale"].cpu() == s).all()
+        assert torch.equal(o["q"].cpu().view(torch.uint8), (w / s).to(torch.float8_e4m3fn).view(torch.uint8).expand(2, D))
