@@ -155,14 +155,16 @@ __device__ __forceinline__ float wave_sum(float x) {
 }
 
 // out(c, sum over r < rows of part[r][c]) for every column c < cols: 64 columns a workgroup, 16
-// waves that each take every 16th row, joined in a fixed order.
+// waves that each take every 16th row, joined in a fixed order.  Added in 64 bits: a long call has
+// many thousands of rows, and a running fp32 sum of n terms of one sign loses up to n / 2 units of
+// 2^-24.
 template <typename Out>
 __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ part, int rows, int64_t cols,
                                                           int64_t first, Out out) {
-  __shared__ float acc[16][64];
+  __shared__ double acc[16][64];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int64_t c = first + (int64_t)blockIdx.x * 64 + lane;
-  float s = 0.f;
+  double s = 0.0;
   if (c < cols) {
 #pragma unroll 4
     for (int r = wv; r < rows; r += 16) s += part[(int64_t)r * cols + c];
@@ -170,10 +172,10 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
   acc[wv][lane] = s;
   __syncthreads();
   if (wv == 0 && c < cols) {
-    float t = acc[0][lane];
+    double t = acc[0][lane];
 #pragma unroll
     for (int i = 1; i < 16; ++i) t += acc[i][lane];
-    out(c, t);
+    out(c, (float)t);
   }
 }
 template <typename Out>

@@ -107,3 +107,21 @@ def test_step(D, W, pitch, dtype):
     state = st.to(DEV)
     g.causal_conv_step(xd[:2], w.to(DEV), state)
     assert torch.equal(state.cpu()[2:], st[2:]) and torch.equal(state.cpu()[1, -1], x[1])
+
+
+def test_weight_sums_of_many_equal_terms():
+    """2^24 tokens of one value a channel: a running fp32 sum of that many equal terms loses up to 2^13 u
+    (u = 2^-24: each addition is off by half a unit of the sum so far).  A tile's 64 terms of 16 bits
+    add up exactly and the tiles' shares are added in 64 bits, so the result is off by its own rounding."""
+    import gated_delta_rule_29_amd as g
+
+    say("conv: sums of 2^24 equal terms")
+    T, D, r = 1 << 24, 16, gen(41)
+    x, dy = ((1 + torch.rand(D, generator=r)).bfloat16() for _ in range(2))
+    o = g.causal_conv_bwd(dy.to(DEV).expand(1, T, D).contiguous(), x.to(DEV).expand(1, T, D).contiguous(),
+                          torch.zeros(D, 4, device=DEV), bias=torch.zeros(D, device=DEV), silu=False)
+    terms = T - 3 + torch.arange(4.0, dtype=torch.float64)  # (the first tokens' windows begin with zeros)
+    for k, ref in (("dbias", T * dy.double()), ("dw", (x.double() * dy.double())[:, None] * terms)):
+        err = float(((o[k].cpu().double() - ref).abs() / ref).max()) * 2 ** 24
+        say("  %s error %.1f u" % (k, err))
+        assert err <= 2
