@@ -79,6 +79,31 @@ struct AddChannels<4, 4> {
   }
 };
 
+// A thread's dA, dskip and ddt_bias over a piece, which may be a whole sequence: a running fp32 sum would
+// lose up to half a unit of 2^-24 for each of its tokens where the terms have one sign, so the registers'
+// sums of kFold tokens are added up here.  Kept in LDS by four lanes a channel, whose registers are all
+// taken (8 of them would spill), in registers by 16, whose LDS is.
+constexpr int kFold = 256;
+template <int LN, int K>
+struct PieceSums {
+  static constexpr int LDS = 1;
+  float s[K] = {};
+  __device__ __forceinline__ PieceSums(float*) {}
+  __device__ __forceinline__ void add(int i, float v) { s[i] += v; }
+  __device__ __forceinline__ float get(int i) const { return s[i]; }
+};
+template <int K>
+struct PieceSums<4, K> {
+  static constexpr int LDS = K * 256;
+  float* s;  // [K][256 threads], each thread its own
+  __device__ __forceinline__ PieceSums(float* lds) : s(lds + threadIdx.x) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) s[i * 256] = 0.f;
+  }
+  __device__ __forceinline__ void add(int i, float v) { s[i * 256] += v; }
+  __device__ __forceinline__ float get(int i) const { return s[i * 256]; }
+};
+
 // A chunk's x, dt, z and dy as a lane owns them: the j-th of every LN tokens of channel cc; 0 behind the
 // end.  (Without a gate z is read as x and not used.)
 template <typename T, int LN>
@@ -198,6 +223,7 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
   __shared__ __align__(16) float bc[2][kSsmChunk * NP * 2];
   __shared__ __align__(16) float red[2][4][kSsmChunk * 2 * NP];
   __shared__ __align__(16) float shares[4][AddChannels<LN, NPL>::LDS];
+  __shared__ float far[PieceSums<LN, NPL + 2>::LDS];
   const SsmParams& f = p.f;
   const Place<LN> w(f, groups, f.split.main, f.split.nmain);
   if (w.pc.seq < 0) return;
@@ -226,6 +252,7 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
   }
   const float bias = f.dt_bias ? f.dt_bias[cc] : 0.f, skip = f.skip ? f.skip[cc] : 0.f;
   float dskip = 0.f, dbias = 0.f;
+  PieceSums<LN, NPL + 2> sums(far);
   const unsigned vo = cv ? (unsigned)(j * f.D + c) * sizeof(T) : kNowhere;
   AddChannels<LN, NPL> add(shares[w.wv], w.lane);
   st.store(bc[0]);
@@ -318,14 +345,24 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdParams p, int gro
         p.part_bc[(((int64_t)w.grp * f.s.rows + tb + k) * 2 + m / NP) * f.N + n] =
             red[buf][0][e] + red[buf][1][e] + red[buf][2][e] + red[buf][3][e];
     }
+    if ((tb - t0) % kFold == 0) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        sums.add(i, dA[i]);
+        dA[i] = 0.f;
+      }
+      sums.add(NPL, dskip);
+      sums.add(NPL + 1, dbias);
+      dskip = dbias = 0.f;
+    }
   }
   if (cv) {
     float* pa = p.part_a + ((int64_t)w.seg * f.D + c) * (f.N + 2);
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
-      if (j * NPL + i < f.N) pa[j * NPL + i] = dA[i];
-    dskip = group_sum<LN>(dskip);
-    dbias = group_sum<LN>(dbias);
+      if (j * NPL + i < f.N) pa[j * NPL + i] = sums.get(i);
+    dskip = group_sum<LN>(sums.get(NPL));
+    dbias = group_sum<LN>(sums.get(NPL + 1));
     if (j == 0) {
       pa[f.N] = dskip;
       pa[f.N + 1] = dbias;

@@ -360,3 +360,29 @@ def test_packed_gradient_of_short_sequences_beside_cut_ones(lens, D, N, full, dt
     u = 2.0 ** -24 * (40 + 1.2 * M ** 0.5 + 0.03 * M)
     for k in o:
         check(k, o[k], ref[k], u * float(np.abs(ref[k]).max() / np.sqrt((ref[k] * ref[k]).mean())))
+
+
+@pytest.mark.parametrize("n,N", [(2048, 2), (512, 20)])  # 4 and 16 lanes a channel
+def test_parameter_sums_of_many_equal_terms(n, N):
+    """Sequences of 16384 tokens, so many that none is cut, alike from token to token: dA, dD and ddt_bias are
+    sums of that many terms of one sign, in which a running fp32 sum loses up to 8192 u.  Here at most
+    256 terms meet in a register and 64 of their sums after that, (256 + 64) / 2 u, beside a term's own
+    40 u and the lanes' 4 u; the sequences' sums are joined in 64 bits."""
+    import gated_delta_rule_29_amd as g
+
+    say("scan: sums of 16384 equal terms, %d sequences, %d states" % (n, N))
+    T, D, r = 16384, 16, gen(43)
+    x, dy = ((1 + torch.rand(D, generator=r)).bfloat16() for _ in range(2))
+    A, bias, skip = -0.5 - torch.rand(D, N, generator=r), torch.rand(D, generator=r) * 0.1, torch.ones(D)
+    line = dict(x=x.expand(T, D), dt=torch.full((T, D), 0.5), Bm=torch.full((T, N), 1.125), Cm=torch.full((T, N), 1.25))
+    d = {k: v.bfloat16().to(DEV).expand(n, *v.shape).contiguous() for k, v in dict(line, dy=dy.expand(T, D)).items()}
+    args = (d["x"], d["dt"], A.to(DEV), d["Bm"], d["Cm"])
+    opt = dict(D=skip.to(DEV), dt_bias=bias.to(DEV), softplus=False)
+    h = g.ssm_scan_fwd(*args, want_ht=False, want_h=True, **opt)["h"]
+    o = g.ssm_scan_bwd(d["dy"], h, *args, **opt)
+    ref = L.scan_bwd([T], arr(dy.expand(T, D)), A=arr(A), skip=arr(skip), dt_bias=arr(bias), use_softplus=False,
+                     **{k: arr(v) for k, v in line.items()})
+    for k in ("dA", "dD", "ddt_bias"):
+        err = float(np.abs(arr(o[k]) / (n * ref[k]) - 1).max()) * 2 ** 24
+        say("  %s error %.1f u" % (k, err))
+        assert err <= 204
