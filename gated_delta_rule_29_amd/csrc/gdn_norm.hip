@@ -229,7 +229,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(NormPar
 }
 
 // The rows of a gradient call are dealt to `groups` row workers (a workgroup, or one of its waves
-// where rows are short); each keeps its share of dw in registers and writes it once.
+// where rows are short); each keeps its share of dw in registers.  A worker of a long call has thousands of
+// rows, and a running fp32 sum of n terms of one sign loses up to n / 2 units of 2^-24: every kFold
+// rows the registers are added to the share in the workspace.
+constexpr int kFold = 64;
 template <typename T, typename RT, int V, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwdParams p, int groups) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
@@ -240,54 +243,71 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(NormBwd
   float* rd = red + sub * (TPR / 64);
   float dw[NV][V] = {};
   const float inv_d = 1.f / (float)p.D;
-  for (int row = worker; row < p.M; row += groups) {
-    const T* dy = static_cast<const T*>(p.dy) + row * p.dy_pitch;
-    const RT* s = static_cast<const RT*>(p.s) + row * p.s_pitch;
-    const float r = p.rstd[row];
-    float g[NV][V], v[NV][V], dot = 0.f;
+  // dw to the workspace: as its first rows' sums, or added to those that are there
+  auto fold = [&](bool first) {
+    int at = tid;
+    asm volatile("" : "+v"(at));  // no instruction; keeps the addresses from holding registers between
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + tid) * V;
+      const int c = (i * TPR + at) * V;
       if (c < p.D) {
-        float w[V];
-        load_vec<T, V>(dy + c, g[i]);
-        load_vec<RT, V>(s + c, v[i]);
-        load_vec<float, V>(p.w + c, w);
+        float* q = p.part + (int64_t)worker * p.D + c;
+        if (!first) {
+          float old[V];
+          load_vec<float, V>(q, old);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          v[i][k] *= r;
-          dw[i][k] = __builtin_fmaf(g[i][k], v[i][k], dw[i][k]);
-          g[i][k] *= w[k];
-          dot = __builtin_fmaf(g[i][k], v[i][k], dot);
+          for (int k = 0; k < V; ++k) dw[i][k] += old[k];
+        }
+        store_vec<float, V>(q, dw[i]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) dw[i][k] = 0.f;
+      }
+    }
+  };
+  for (int first = worker; first < p.M; first += kFold * groups) {
+    const int end = min(p.M, first + kFold * groups);
+    for (int row = first; row < end; row += groups) {
+      const T* dy = static_cast<const T*>(p.dy) + row * p.dy_pitch;
+      const RT* s = static_cast<const RT*>(p.s) + row * p.s_pitch;
+      const float r = p.rstd[row];
+      float g[NV][V], v[NV][V], dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + tid) * V;
+        if (c < p.D) {
+          float w[V];
+          load_vec<T, V>(dy + c, g[i]);
+          load_vec<RT, V>(s + c, v[i]);
+          load_vec<float, V>(p.w + c, w);
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            v[i][k] *= r;
+            dw[i][k] = __builtin_fmaf(g[i][k], v[i][k], dw[i][k]);
+            g[i][k] *= w[k];
+            dot = __builtin_fmaf(g[i][k], v[i][k], dot);
+          }
+        }
+      }
+      dot = row_sum<TPR>(dot, rd) * inv_d;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + tid) * V;
+        if (c < p.D) {
+          float o[V];
+#pragma unroll
+          for (int k = 0; k < V; ++k) o[k] = r * (g[i][k] - v[i][k] * dot);
+          if (p.dsum) {
+            float d[V];
+            load_vec<RT, V>(static_cast<const RT*>(p.dsum) + row * p.dsum_pitch + c, d);
+#pragma unroll
+            for (int k = 0; k < V; ++k) o[k] += d[k];
+          }
+          store_vec<RT, V>(static_cast<RT*>(p.dres) + (int64_t)row * p.D + c, o);
+          if (p.dx) store_vec<T, V>(static_cast<T*>(p.dx) + (int64_t)row * p.D + c, o);
         }
       }
     }
-    dot = row_sum<TPR>(dot, rd) * inv_d;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * TPR + tid) * V;
-      if (c < p.D) {
-        float o[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) o[k] = r * (g[i][k] - v[i][k] * dot);
-        if (p.dsum) {
-          float d[V];
-          load_vec<RT, V>(static_cast<const RT*>(p.dsum) + row * p.dsum_pitch + c, d);
-#pragma unroll
-          for (int k = 0; k < V; ++k) o[k] += d[k];
-        }
-        store_vec<RT, V>(static_cast<RT*>(p.dres) + (int64_t)row * p.D + c, o);
-        if (p.dx) store_vec<T, V>(static_cast<T*>(p.dx) + (int64_t)row * p.D + c, o);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * TPR + tid) * V;
-    if (c < p.D) {
-#pragma unroll
-      for (int k = 0; k < V; ++k) p.part[(int64_t)worker * p.D + c + k] = dw[i][k];
-    }
+    fold(first == worker);
   }
 }
 

@@ -165,3 +165,21 @@ def test_eight_bits_round_the_quotient(D, block):
         o = g.rms_norm_q8_fwd(torch.ones(2, D, device=DEV), w.to(DEV), eps=1e-30, block=block)
         assert (o["scale"].cpu() == s).all()
         assert torch.equal(o["q"].cpu().view(torch.uint8), (w / s).to(torch.float8_e4m3fn).view(torch.uint8).expand(2, D))
+
+
+@pytest.mark.parametrize("D,M", [(16, 1 << 24), (15, 1 << 24), (520, 1 << 22)])
+def test_weight_gradient_of_many_equal_terms(D, M):
+    """4096 rows a worker, all alike: dw's terms have one sign, and a running fp32 sum of 4096 of them loses
+    up to 2048 u.  Here 64 terms meet in a register and 64 of their sums after that, (64 + 64) / 2 u; the
+    workers' shares are added in 64 bits, and rstd and a term are off by 4 u."""
+    import gated_delta_rule_29_amd as g
+
+    say("norm: sums of equal terms, %d rows of %d" % (M, D))
+    dy = 1 + torch.rand(D, generator=gen(D))
+    s = torch.ones(M, D, device=DEV)
+    rstd = g.rms_norm_fwd(s, torch.ones(D, device=DEV), want_rstd=True)["rstd"]
+    o = g.rms_norm_bwd(dy.to(DEV).expand(M, D).contiguous(), s, torch.ones(D, device=DEV), rstd)
+    ref = M * dy.double() / (1 + EPS) ** 0.5
+    err = float(((o["dw"].cpu().double() - ref).abs() / ref).max()) * 2 ** 24
+    say("  error %.1f u" % err)
+    assert err <= 68
