@@ -102,6 +102,13 @@ def _call(name, dev, *args):
         _lib.check(rc, name)
 
 
+_INT = 0x7fffffff  # the library's sizes are 32-bit integers: ctypes would pass on the low bits of larger ones
+
+
+def _large(*sizes):
+    raise ValueError("sizes beyond 32 bits: %s" % (sizes,))
+
+
 _CPU = torch.device("cpu")
 
 
@@ -122,6 +129,8 @@ class _Seqs:
     """The sequences of a call: a dense batch, or the offsets of a packed one."""
 
     def __init__(self, x, cu_seqlens=None, cu_seqlens_host=None):
+        if x.shape[0] * x.shape[1] > _INT or x.shape[2] > _INT:
+            _large(x.shape[0] * x.shape[1], x.shape[2])
         self.packed = cu_seqlens is not None
         if self.packed:
             if x.shape[0] != 1:
@@ -167,6 +176,8 @@ def _conv_fwd(x, w, bias, init, silu, want_last, cu=None, cu_host=None):
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a [D, W] tensor")
     W = w.shape[1]
+    if W > _INT:
+        _large(W)
     pitch = _rows(x, "x", x.shape, dt, dev)
     wp, bp = _need(w, "w", (D, W), F32, dev), _need(bias, "bias", (D,), F32, dev)
     edge = (seqs.n, max(W - 1, 0), D)
@@ -202,6 +213,8 @@ def _conv_bwd(dy, x, w, bias, init, dfinal, silu, cu=None, cu_host=None):
     if not isinstance(w, torch.Tensor) or w.dim() != 2:
         raise ValueError("w must be a [D, W] tensor")
     W = w.shape[1]
+    if W > _INT:
+        _large(W)
     pitch, dy_pitch = _rows(x, "x", x.shape, dt, dev), _rows(dy, "dy", x.shape, dt, dev)
     _need(w, "w", (D, W), F32, dev)
     _need(bias, "bias", (D,), F32, dev)
@@ -252,6 +265,8 @@ def causal_conv_step(x, w, state, bias=None, *, slots=None, silu=True):
     if not isinstance(w, torch.Tensor) or w.dim() != 2 or not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError("w must be a [D, W] and state a [S, W-1, D] tensor")
     W, S = w.shape[1], state.shape[0]
+    if B > _INT or S > _INT or D > _INT or W > _INT:
+        _large(B, S, D, W)
     pitch = _rows(x, "x", x.shape, dt, dev)
     wp, bp = _need(w, "w", (D, W), F32, dev), _need(bias, "bias", (D,), F32, dev)
     sp = _need(state, "state", (S, max(W - 1, 0), D), dt, dev)
@@ -270,6 +285,8 @@ def _scan_args(x, dt_, A, Bm, Cm, skip, z, dt_bias, dev, dt):
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be a [D, N] tensor")
     N = A.shape[1]
+    if D > _INT or N > _INT:
+        _large(D, N)
     shape, per_n = x.shape, (*lead, N)
     px, pd = _rows(x, "x", shape, dt, dev), _rows(dt_, "dt", shape, dt, dev)
     ap = _need(A, "A", (D, N), F32, dev)
@@ -384,6 +401,8 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, slots=Non
         raise ValueError("state must be a [S, C, N] tensor")
     N, ins, opts = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, dev, ty)
     S = state.shape[0]
+    if B > _INT or S > _INT:
+        _large(B, S)
     sp = _need(state, "state", (S, C, N), F32, dev)
     lp = _slots(state, slots, B, dev)
     y = _like(x)
@@ -399,6 +418,9 @@ def _norm_args(x, w, residual):
     dev, dt, code = _act(x, "x", x.dim())
     shape = x.shape
     D = shape[-1]
+    M = x.numel() // max(D, 1)
+    if M > _INT or D > _INT:
+        _large(M, D)
     pitch = _rows(x, "x", shape, dt, dev)
     wp = _need(w, "w", (D,), F32, dev)
     rcode, rpitch, rp = code, 0, None
@@ -407,7 +429,7 @@ def _norm_args(x, w, residual):
             raise ValueError("residual must be a float32 or bfloat16 tensor")
         rcode = _DT[residual.dtype]
         rp, rpitch = residual.data_ptr(), _rows(residual, "residual", shape, residual.dtype, dev)
-    return dev, code, rcode, D, x.numel() // max(D, 1), (x.data_ptr(), pitch, rp, rpitch, wp)
+    return dev, code, rcode, D, M, (x.data_ptr(), pitch, rp, rpitch, wp)
 
 
 def rms_norm_fwd(x, w, residual=None, eps=1e-5, *, want_rstd=False):
@@ -455,6 +477,9 @@ def rms_norm_bwd(dy, s, w, rstd, dsum=None):
         raise ValueError("dy must be a tensor [.., D]")
     dev, dt, code = _act(dy, "dy", dy.dim())
     D = dy.shape[-1]
+    M = dy.numel() // max(D, 1)
+    if M > _INT or D > _INT:
+        _large(M, D)
     if not isinstance(s, torch.Tensor) or s.dtype not in _DT:
         raise ValueError("s must be a float32 or bfloat16 tensor")
     pitch, s_pitch = _rows(dy, "dy", dy.shape, dt, dev), _rows(s, "s", dy.shape, s.dtype, dev)
@@ -463,7 +488,6 @@ def rms_norm_bwd(dy, s, w, rstd, dsum=None):
     if rstd is None:
         raise ValueError("rstd is needed: rms_norm_fwd gives it with want_rstd")
     _need(rstd, "rstd", dy.shape[:-1], F32, dev)
-    M = dy.numel() // max(D, 1)
     ds = _like(s)
     dx = ds if s.dtype == dt else _like(dy)
     dw = torch.empty_like(w)

@@ -239,3 +239,25 @@ def test_pitches_of_views():
     assert _rows(wide[..., 5:6], "x", (3, 4, 1), torch.float32, cpu) == 20
     with pytest.raises(ValueError):
         _rows(wide[:, :3, 2:10], "x", (3, 3, 8), torch.float32, cpu)  # batches are further apart
+
+
+def test_sizes_beyond_32_bits():
+    """Refused before the library, which would see their low bits.  (Meta tensors: no memory.)"""
+    import gated_delta_rule_29_amd as g
+
+    big = (1 << 32) + 4
+    t = lambda *s: torch.empty(s, device="meta")  # noqa: E731
+    x, w, A, bc, v = t(1, big, 1), t(1, 4), t(1, 4), t(1, big, 4), t(1)
+    for bad in (lambda: g.causal_conv_fwd(x, w), lambda: g.causal_conv_bwd(x, x, w),
+                lambda: g.causal_conv_fwd(t(1 << 17, 1 << 16, 1), w),
+                lambda: g.causal_conv_fwd_varlen(x, w, torch.tensor([0, 4], dtype=torch.int32)),
+                lambda: g.causal_conv_fwd(t(1, 4, 1), t(1, big)), lambda: g.causal_conv_bwd(t(1, 4, 1), t(1, 4, 1), t(1, big)),
+                lambda: g.causal_conv_step(x[0], w, t(4, 3, 1), slots=torch.empty(big, dtype=torch.int32, device="meta")),
+                lambda: g.causal_conv_step(t(2, 1), w, t(big, 3, 1)),
+                lambda: g.ssm_scan_fwd(x, x, A, bc, bc), lambda: g.ssm_scan_fwd(t(1, 4, 1), t(1, 4, 1), t(1, big), t(1, 4, big), t(1, 4, big)),
+                lambda: g.ssm_scan_bwd(x, t(1, big // 16 + 1, 1, 4), x, x, A, bc, bc),
+                lambda: g.ssm_step(t(2, 1), t(2, 1), A, t(2, 4), t(2, 4), t(big, 1, 4)),
+                lambda: g.ssm_step(x[0], x[0], A, bc[0], bc[0], t(big, 1, 4)),
+                lambda: g.rms_norm_fwd(x, v), lambda: g.rms_norm_q8_fwd(x, v), lambda: g.rms_norm_bwd(x, x, v, x[..., 0])):
+        with pytest.raises(ValueError, match="32 bits"):
+            bad()
