@@ -125,14 +125,19 @@ def _workspace(nbytes, dev):
     return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
 
 
+_DENSE = object()  # in the place of a dense call's offsets
+
+
 class _Seqs:
     """The sequences of a call: a dense batch, or the offsets of a packed one."""
 
-    def __init__(self, x, cu_seqlens=None, cu_seqlens_host=None):
+    def __init__(self, x, cu_seqlens=_DENSE, cu_seqlens_host=None):
         if x.shape[0] * x.shape[1] > _INT or x.shape[2] > _INT:
             _large(x.shape[0] * x.shape[1], x.shape[2])
-        self.packed = cu_seqlens is not None
+        self.packed = cu_seqlens is not _DENSE
         if self.packed:
+            if cu_seqlens is None:
+                raise ValueError("a packed call needs cu_seqlens")
             if x.shape[0] != 1:
                 raise ValueError("packed input must have batch 1, got %d" % x.shape[0])
             if _int32(cu_seqlens, x.device) and _int32(cu_seqlens_host, _CPU) \
@@ -169,7 +174,7 @@ class _Seqs:
 
 # ----------------------------------------------------------------------------------- convolution
 
-def _conv_fwd(x, w, bias, init, silu, want_last, cu=None, cu_host=None):
+def _conv_fwd(x, w, bias, init, silu, want_last, cu=_DENSE, cu_host=None):
     dev, dt, code = _act(x, "x", 3)
     seqs = _Seqs(x, cu, cu_host)
     D = x.shape[2]
@@ -206,7 +211,7 @@ def causal_conv_fwd_varlen(x, w, cu_seqlens, bias=None, init=None, *, silu=True,
     return _conv_fwd(x, w, bias, init, silu, want_final, cu_seqlens, cu_seqlens_host)
 
 
-def _conv_bwd(dy, x, w, bias, init, dfinal, silu, cu=None, cu_host=None):
+def _conv_bwd(dy, x, w, bias, init, dfinal, silu, cu=_DENSE, cu_host=None):
     dev, dt, code = _act(x, "x", 3)
     seqs = _Seqs(x, cu, cu_host)
     D = x.shape[2]
@@ -303,7 +308,7 @@ def _scan_workspace(which, seqs, x, N):
     return getattr(lib, "ssm_scan_%s_workspace_bytes" % which)(x.shape[0], x.shape[1], D, N)
 
 
-def _scan_fwd(x, dt, A, Bm, Cm, skip, z, dt_bias, h0, softplus, want_ht, want_h, cu=None, cu_host=None):
+def _scan_fwd(x, dt, A, Bm, Cm, skip, z, dt_bias, h0, softplus, want_ht, want_h, cu=_DENSE, cu_host=None):
     dev, ty, code = _act(x, "x", 3)
     seqs = _Seqs(x, cu, cu_host)
     N, ins, opts = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, dev, ty)
@@ -343,7 +348,7 @@ def ssm_scan_fwd_varlen(x, dt, A, Bm, Cm, cu_seqlens, D=None, z=None, dt_bias=No
     return _scan_fwd(x, dt, A, Bm, Cm, D, z, dt_bias, h0, softplus, want_ht, want_h, cu_seqlens, cu_seqlens_host)
 
 
-def _scan_bwd(dy, h, x, dt, A, Bm, Cm, skip, z, dt_bias, dht, softplus, want_dh0, cu=None, cu_host=None):
+def _scan_bwd(dy, h, x, dt, A, Bm, Cm, skip, z, dt_bias, dht, softplus, want_dh0, cu=_DENSE, cu_host=None):
     dev, ty, code = _act(x, "x", 3)
     seqs = _Seqs(x, cu, cu_host)
     N, ins, opts = _scan_args(x, dt, A, Bm, Cm, skip, z, dt_bias, dev, ty)

@@ -261,3 +261,16 @@ def test_sizes_beyond_32_bits():
                 lambda: g.rms_norm_fwd(x, v), lambda: g.rms_norm_q8_fwd(x, v), lambda: g.rms_norm_bwd(x, x, v, x[..., 0])):
         with pytest.raises(ValueError, match="32 bits"):
             bad()
+
+
+def test_packed_calls_without_offsets():
+    """None in the place of the offsets is refused, not taken for a dense batch."""
+    import gated_delta_rule_29_amd as g
+
+    x, w, A, bc = torch.zeros(1, 5, 8), torch.zeros(8, 4), torch.zeros(8, 16), torch.zeros(1, 5, 16)
+    for bad in (lambda: g.causal_conv_fwd_varlen(x, w, None), lambda: g.causal_conv_bwd_varlen(x, x, w, None),
+                lambda: g.causal_conv_fwd_varlen(x, w, None, cu_seqlens_host=torch.tensor([0, 5], dtype=torch.int32)),
+                lambda: g.ssm_scan_fwd_varlen(x, x, A, bc, bc, None),
+                lambda: g.ssm_scan_bwd_varlen(x, torch.zeros(1, 1, 8, 16), x, x, A, bc, bc, None)):
+        with pytest.raises(ValueError, match="cu_seqlens"):
+            bad()
