@@ -7,9 +7,10 @@
 //   ds = r (dy w - s r^2 mean(dy w s)) + dsum,   dw_c = sum over rows of dy_c s_c r
 //
 // One row's values stay in the registers of TPR threads: every input is read once, and the kernels run at
-// the rate of a large copy (5.2 TB/s): 16384 rows of 4096 bf16 with a bf16 residual 89 us (537 MB) and
-// their gradient 111 us (537 MB and 17 MB of weight-gradient shares); 8192 rows of 4096 with an fp32
-// residual to 8 bits in 128-column blocks 71 us (370 MB).  A single row takes 2.6 us.
+// the rate of a large copy (5.2 TB/s) or above it: 16384 rows of 4096 bf16 with a bf16 residual 90 us (537 MB:
+// 6.0 TB/s, part of which the 256 MB cache takes) and their gradient 112 us (537 MB and 17 MB of
+// weight-gradient shares: 4.9 TB/s); 8192 rows of 4096 with an fp32 residual to 8 bits in 128-column blocks
+// 72 us (370 MB: 5.2 TB/s).  A single row takes 2.6 us.
 #include "../../include/gdn.h"
 #include "gdn_layer_device.h"
 
@@ -319,7 +320,9 @@ struct NormWeightOut {
 bool al16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Threads of a row and vectors of a thread: 64 threads for short rows, 256 for up to 8192 columns
-// in 16-byte vectors, 1024 beyond that and for single columns.
+// in 16-byte vectors, 1024 beyond that and for single columns.  (The gradient's registers do not hold its
+// widest instances: beyond 16384 columns 7 to 12 are spilled, of more than 4096 single columns 54 to 56:
+// 4096 rows of 4097 bf16 take 104 us, 1 TB/s.)
 template <typename F>
 hipError_t by_width(int D, bool vec, F&& f) {
   using std::integral_constant;

@@ -226,13 +226,17 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmStepParams p, int grou
 }  // namespace
 
 // Long sequences are cut where the channels give fewer than two waves a SIMD (2048): the summary costs
-// 0.6 of the scan proper, less than what too few waves cost.  Segments are then as short as gives
-// eight waves a SIMD.  4 sequences of 2048 tokens x 4096 channels x 16 states (scan + summary, us; with an
-// earlier form of the scan): uncut, one wave, 276; cut for two 212 + 122, for four 187 + 108, for
-// eight 179 + 102.  Two waves uncut: 212 by the same row.
+// 0.65 of the scan proper, less than what too few waves cost.  Segments are then as short as gives
+// eight waves a SIMD.  Sequences of 2048 tokens x 4096 channels x 16 states, bf16 (scan + summary, us): four
+// of them uncut, one wave, 303; cut for two 201 + 124, for four 173 + 109, for eight 161 + 106.  Eight of them
+// uncut, two waves, 398; cut for eight 307 + 194.
 //
-// The gradient's registers allow two waves a SIMD and no more, so that it takes pieces of several
-// segments, and only what is behind the first piece has to be summarised.
+// The gradient's registers allow two waves a SIMD (three with 17 to 32 states), so that it takes pieces of
+// several segments, and only what is behind the first piece has to be summarised: four of those sequences
+// uncut 752 us, in two-wave segments 513 + 164, in pieces of eight-wave segments 520 + 71.
+//
+// The rule takes sequences for equally long.  One of 16384 tokens beside eight of one token counts as nine
+// and is not cut: 2337 us, against 550 by itself.
 SsmSplit ssm_split(bool backward, const int* cu, int n, int T, int D, int N) {
   const int ch = ssm_channels(N) / 4;  // channels of a wave
   const int64_t per_seg = (D + ch - 1) / ch;

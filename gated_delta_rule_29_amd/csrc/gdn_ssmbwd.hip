@@ -211,8 +211,8 @@ __global__ __launch_bounds__(256) void ssm_bwd_join_kernel(SsmBwdParams p, int p
 
 // The gradient proper.  Bound by vector instructions: 56 of the 94 a token and wave are its own (4 states
 // a lane, 14 operations each, one of them an exponential).  4 x 2048 tokens x 4096 channels x 16 states,
-// bf16: 500 us, vector units busy 62% of the time.  What the layout costs and gains there:
-//  - 16 tokens' a and a h in registers (128 of the 250) leave two waves a SIMD.  32 tokens of a h with
+// bf16: 520 us, vector units busy 69% of the time.  What the layout costs and gains there:
+//  - 16 tokens' a and a h in registers (128 of the 255) leave two waves a SIMD.  32 tokens of a h with
 //    the exponential taken again spilled 61 registers: 1290 us.
 //  - the channel sums through LDS: 640 us with two barriers a chunk, 572 with one.
 //  - the next chunk's inputs asked for in the middle of the walk, when the last group's a and a h are

@@ -640,7 +640,8 @@ GDN_API int gdn_bwd_dhu_varlen(const void* q, const void* k, const void* w, cons
  *    beyond; of 256 in a convolution's step): GDN_ERR_INVALID; pitches beyond GDN_MAX_PITCH are
  *    GDN_ERR_UNSUPPORTED (32 rows are addressed with 32-bit offsets).
  *  - dtype is that of the activations (inputs and outputs that are not said to be fp32);
- *    all arithmetic, states and sums over tokens or channels are fp32, each result rounded once.
+ *    all arithmetic, states and sums over tokens or channels are fp32 (the sums' shares of different
+ *    workgroups are added in fp64), each result rounded once.
  *  - Pointers have their type's alignment; 16-byte alignment (and pitches and widths that are
  *    multiples of 16 bytes) is faster.  fp32 [.., D, N] tensors (A, states) must be 16-byte
  *    aligned where N is a multiple of 4.
