@@ -217,6 +217,7 @@ def prepare(case, seed):
     s["lens"] = torch.tensor(keys, dtype=torch.int32, device=DEV)
     s["q"] = torch.randn(sum(new), case["Hq"], case["D"], generator=gen, device=DEV).to(t)
     if op == "attn":
+        s["q"] = s["q"][None]  # a packed batch
         s["cu_host"] = torch.tensor([0] + new, dtype=torch.int32).cumsum(0).to(torch.int32)
         s["cu"] = s["cu_host"].to(DEV)
     return s
@@ -315,7 +316,8 @@ def _plain_chunks(s):
     case = s["case"]
     Hk, D, P, G = case["Hk"], case["D"], case["P"], case["Hq"] // case["Hk"]
     new, keys = _seqs(case)
-    o = torch.zeros(s["q"].shape, device=DEV)
+    queries = s["q"][0]
+    o = torch.zeros(queries.shape, device=DEV)
     t0 = 0
     for i, (n, L) in enumerate(zip(new, keys)):
         if L:
@@ -324,7 +326,7 @@ def _plain_chunks(s):
             k, v = (_gather(s, name, page, at % P).transpose(0, 1).contiguous() for name in ("k", "v"))
             step = max(1, (1 << 28) // (L * Hk * G))
             for r in range(0, n, step):
-                q = s["q"][t0 + r:t0 + min(n, r + step)].float()
+                q = queries[t0 + r:t0 + min(n, r + step)].float()
                 m = q.shape[0]
                 q = q.view(m, Hk, G, D).permute(1, 2, 0, 3).reshape(Hk, G * m, D)
                 if case["causal"]:
@@ -337,7 +339,7 @@ def _plain_chunks(s):
                 part = _attend(q, k, v, seen.repeat(G, 1))
                 o[t0 + r:t0 + r + m] = part.view(Hk, G, m, D).permute(2, 0, 1, 3).reshape(m, Hk * G, D)
         t0 += n
-    return {"o": o.to(s["q"].dtype)}
+    return {"o": o.to(s["q"].dtype)[None]}
 
 
 # ------------------------------------------------------------------------------ the library's calls
@@ -463,7 +465,7 @@ def _exact_attn(case, s):
     """Head by head, each query's weights over the keys that it sees."""
     new, keys = _seqs(case)
     D, P, G = case["D"], case["P"], case["Hq"] // case["Hk"]
-    q = s["q"].double()
+    q = s["q"].double().view(-1, case["Hq"], D)
     o = torch.zeros_like(q)
     t0 = 0
     for i, (n, L) in enumerate(zip(new, keys)):
@@ -488,7 +490,7 @@ def _exact_attn(case, s):
                     w = torch.softmax(z, -1)
                     o[t0 + a:t0 + b, g] = torch.nan_to_num(w) @ v  # a row without keys: 0
         t0 += n
-    return {"o": o}
+    return {"o": o.view(s["q"].shape)}
 
 
 def exact(case, seed):
