@@ -829,3 +829,8 @@ from . import layer  # noqa: E402  (it takes this module's helpers)
 from .layer import *  # noqa: E402,F401,F403
 
 __all__ += layer.__all__
+
+from . import attention  # noqa: E402
+from .attention import *  # noqa: E402,F401,F403
+
+__all__ += attention.__all__

@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgdn.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = 0, 1, 2, 3, 4
-DTYPE_F32, DTYPE_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_E4M3 = 0, 1, 2
 FWD_PER_KEY, FWD_SAVES = 1, 2
 BWD_ACCUMULATE = 2
 BWD_REUSE_STATS = 4
@@ -94,6 +94,17 @@ SIGNATURES = {
     "rms_norm_q8_fwd": (I, [P, L, P, L, P, F, I, P, P, P, I, I, I, I, P]),
     "rms_norm_bwd_workspace_bytes": (SZ, [I, I]),
     "rms_norm_bwd": (I, [P, L, P, L, P, P, P, L, P, P, P, I, I, I, I, P, SZ, P]),
+    # full-attention layers
+    "rope_fwd": (I, [P, L, L, P, P, F, P, I, I, I, I, I, I, P]),
+    "rope_bwd": (I, [P, L, L, P, P, F, P, I, I, I, I, I, I, P]),
+    "kv_cache_write": (I, [P, L, L, P, L, L, P, P, P, P, P, I, I, I, I, I, I, I, P]),
+    "kv_cache_read": (I, [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]),
+    "paged_attn_workspace_bytes": (SZ, [I, I, I, I, I, I, I, I]),
+    "paged_attn_varlen_workspace_bytes": (SZ, [P, I, I, I, I, I, I, I]),
+    "paged_attn_fwd": (I, [P, L, L, P, P, P, P, P, L, I, P, F, I, I, P, P] + [I] * 9 + [P, SZ, P]),
+    "paged_attn_fwd_varlen": (I, [P, L, L, P, P, P, P, P, L, I, P, P, P, I, F, I, I, P, P] + [I] * 8
+                              + [P, SZ, P]),
+    "paged_attn_step": (I, [P, L, L, P, P, P, P, P, L, I, P, F, I, P] + [I] * 8 + [P, SZ, P]),
 }
 
 _lib = None

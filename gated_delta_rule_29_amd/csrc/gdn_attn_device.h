@@ -1,0 +1,243 @@
+// gdn_attn_device.h -- device-side pieces shared by the attention kernels: the unit of work that a workgroup
+// takes, the keys that a row sees, and what a workgroup's waves leave behind.
+#pragma once
+
+#include "gdn_attn.h"
+#include "gdn_dma.h"
+#include "gdn_layer_device.h"
+
+namespace gdn {
+
+// A piece of a unit's keys.
+struct Unit {
+  int seq, tile;        // tile: row0 / rows of a tile
+  int piece, pieces;    // of the unit
+  int slot;             // number of the piece among all pieces (of a unit's first piece: with piece 0)
+  int begin, n;         // the sequence's first row in the batch and its tokens
+  int len;              // its keys
+  int row0, nrows;      // the unit's rows
+  int lo, hi;           // the piece's keys; lo is a multiple of 64
+};
+
+__device__ __forceinline__ int attn_len(const AttnParams& p, int i) {
+  return min(max(p.lens[i], 0), p.width << p.pshift);
+}
+// New tokens of sequence i (offsets on the device that are not the host's may decrease).
+__device__ __forceinline__ int attn_tokens(const AttnParams& p, int i) {
+  return max(seq_begin(p.s, i + 1) - seq_begin(p.s, i), 0);
+}
+// Tiles of a sequence in the launch's class, and an upper bound of a tile's keys.
+__device__ __forceinline__ int attn_tiles(const AttnParams& p, int rows) {
+  if (p.cls != kAllRows && (rows <= kFewRows) != (p.cls == kFew)) return 0;
+  return (rows + p.plan.rows - 1) / p.plan.rows;
+}
+__device__ __forceinline__ int attn_span(const AttnParams& p, int len) {
+  if (!p.window) return len;
+  const int64_t w = (int64_t)p.window + (p.plan.rows + p.G - 1) / p.G + 64;
+  return (int)min((int64_t)len, w);
+}
+
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Pieces have this many keys at least: so many that the units are cut into `spare` pieces more than there are
+// units.  Every wave of every workgroup finds the same number, by itself.
+__device__ __forceinline__ int attn_piece_keys(const AttnParams& p, int lane) {
+  if (p.plan.spare == 0) return 0x7fffffc0;
+  int64_t sum = 0;
+  for (int i = lane; i < p.s.n; i += 64) {
+    sum += (int64_t)attn_tiles(p, attn_tokens(p, i) * p.G) * attn_span(p, attn_len(p, i));
+  }
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off, 64);
+  int64_t keys = (sum + p.plan.spare - 1) / p.plan.spare;
+  if (keys < p.plan.min_piece) keys = p.plan.min_piece;
+  return uni((int)min((keys + 63) & ~int64_t{63}, int64_t{0x7fffffc0}));
+}
+
+// Finds piece number `id` (PIECES) or the first piece of unit number `id`; false beyond the last one.
+template <bool PIECES>
+__device__ __forceinline__ bool find_unit(const AttnParams& p, int id, int lane, Unit* u) {
+  const int keys = attn_piece_keys(p, lane);
+  int before_t = 0, before_p = 0;  // tiles and pieces of the sequences looked at
+  int seq = -1, tiles_at = 0, pieces_at = 0, per_tile = 1;
+  if (p.plan.spare == 0 && !p.s.cu) {  // sequences alike
+    const int tiles = (p.s.T * p.G + p.plan.rows - 1) / p.plan.rows;
+    seq = id / tiles;
+    if (seq >= p.s.n) return false;
+    tiles_at = pieces_at = seq * tiles;
+  } else {
+    for (int base = 0; base < p.s.n && seq < 0; base += 64) {
+      const int i = base + lane;
+      int tiles = 0, k = 1;
+      if (i < p.s.n) {
+        tiles = attn_tiles(p, attn_tokens(p, i) * p.G);
+        if (p.plan.spare) k = max(1, (attn_span(p, attn_len(p, i)) + keys - 1) / keys);
+      }
+      int it = tiles, ip = tiles * k;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int a = __shfl_up(it, off, 64), b = __shfl_up(ip, off, 64);
+        if (lane >= off) {
+          it += a;
+          ip += b;
+        }
+      }
+      const int here = PIECES ? ip : it, mine = PIECES ? tiles * k : tiles, before = PIECES ? before_p : before_t;
+      const unsigned long long m = __ballot(id < before + here && id >= before + here - mine);
+      if (m) {
+        const int l = __builtin_ctzll(m);
+        seq = base + l;
+        per_tile = uni(__shfl(k, l, 64));
+        tiles_at = before_t + uni(__shfl(it - tiles, l, 64));
+        pieces_at = before_p + uni(__shfl(ip - tiles * k, l, 64));
+      }
+      before_t += uni(__shfl(it, 63, 64));
+      before_p += uni(__shfl(ip, 63, 64));
+    }
+    if (seq < 0) return false;
+  }
+  seq = uni(seq);
+  const int off = PIECES ? id - pieces_at : (id - tiles_at) * per_tile;
+  u->seq = seq;
+  u->pieces = per_tile;
+  u->tile = off / per_tile;
+  u->piece = off - u->tile * per_tile;
+  u->slot = pieces_at + off;
+  u->begin = uni(seq_begin(p.s, seq));
+  u->n = uni(attn_tokens(p, seq));
+  u->len = uni(attn_len(p, seq));
+  u->row0 = u->tile * p.plan.rows;
+  u->nrows = min(p.plan.part_rows, u->n * p.G - u->row0);  // (part_rows: the most that a tile has)
+  // the keys that any of the rows sees, and this piece's share of them
+  int base = 0, end = u->len;
+  if (p.causal) {
+    end = max(0, min(end, u->len - u->n + (u->row0 + u->nrows - 1) / p.G + 1));
+    if (p.window) base = min(end, max(0, u->len - u->n + u->row0 / p.G - p.window + 1)) & ~63;
+  }
+  const int share = ((end - base + per_tile - 1) / per_tile + 63) & ~63;
+  const int64_t lo = base + (int64_t)u->piece * share;
+  u->lo = (int)min(lo, (int64_t)end);
+  u->hi = (int)min(lo + share, (int64_t)end);
+  return true;
+}
+
+// The last key that row `row` of the unit's sequence sees, and the first.
+__device__ __forceinline__ int last_key(const AttnParams& p, const Unit& u, int row) {
+  return p.causal ? min(u.len - 1, u.len - u.n + row / p.G) : u.len - 1;
+}
+__device__ __forceinline__ int first_key(const AttnParams& p, int last) {
+  return p.window ? max(0, last - p.window + 1) : 0;  // (an empty row's last key is negative)
+}
+
+// A cache's rows [key, key + rows) of a head, which lie in one page, as a bounds-checked window: rows at or
+// behind `end`, and pages that the cache does not have, read as zeros.  `row`: bytes.
+struct Window {
+  int64_t at;      // byte offset in the cache
+  uint32_t bytes;
+};
+__device__ __forceinline__ Window page_rows(const AttnParams& p, int seq, int h, int key, int rows, int end,
+                                            int row) {
+  Window w{0, 0};
+  if (key < end) {
+    const int page = p.table[seq * p.table_pitch + (key >> p.pshift)];
+    if (page >= 0 && page < p.pages) {
+      w.at = (((int64_t)page * p.Hk + h) * p.P + (key & (p.P - 1))) * row;
+      w.bytes = (uint32_t)(min(rows, end - key) * row);
+    }
+  }
+  return w;
+}
+
+__device__ __forceinline__ float max_rows16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+__device__ __forceinline__ float max_halves(float x) {
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
+// Which of 8 bf16 values are infinite or NaN, and those values with them set to 0.
+typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ bool not_finite(const bf16x8& v) {
+  const u16x8 b = __builtin_bit_cast(u16x8, v);
+  bool r = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r |= (b[i] & 0x7f80) == 0x7f80;
+  return r;
+}
+__device__ __forceinline__ bf16x8 finite_part(const bf16x8& v) {
+  u16x8 b = __builtin_bit_cast(u16x8, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = (b[i] & 0x7f80) == 0x7f80 ? 0 : b[i];
+  return __builtin_bit_cast(bf16x8, b);
+}
+// Weight of a partial result whose maximum is m in a whole whose maximum is top (both may be -infinity).
+__device__ __forceinline__ float part_weight(float m, float top) {
+  return m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - top);
+}
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -__builtin_inff();
+}
+
+// Index of output row (token of the batch, query head) of the unit's row.
+__device__ __forceinline__ int64_t out_row(const AttnParams& p, const Unit& u, int h, int row) {
+  const int t = row / p.G;
+  return (int64_t)(u.begin + t) * p.Hq + h * p.G + (row - t * p.G);
+}
+// Partial results of a piece: its rows' outputs, and their maxima and sums.
+__device__ __forceinline__ float* part_outputs(const AttnParams& p, int slot, int h) {
+  return p.part + ((int64_t)slot * p.Hk + h) * p.plan.part_rows * p.D;
+}
+__device__ __forceinline__ float* part_sums(const AttnParams& p, int slot, int h) {
+  const int64_t before = (int64_t)(p.plan.units + p.plan.spare) * p.Hk * p.plan.part_rows * p.D;
+  return p.part + before + ((int64_t)slot * p.Hk + h) * p.plan.part_rows * 2;
+}
+
+// The end of a workgroup of WV waves that each have their own keys: col (0 .. ROWS - 1) of wave w has outputs
+// o[w][col][D] (a pitch of D + 4), maximum ml[w][col][0] and sum ml[w][col][1].  Called by all threads,
+// with the waves' values in LDS.
+template <typename T, int D, int ROWS, int WV>
+__device__ __forceinline__ void join_waves(const AttnParams& p, const Unit& u, int h, const float* o,
+                                           const float* ml) {
+  constexpr int LP = D / 4;
+  const bool whole = u.pieces == 1;
+  float* part = whole ? nullptr : part_outputs(p, u.slot, h);
+  float* sums = whole ? nullptr : part_sums(p, u.slot, h);
+  for (int i = threadIdx.x; i < u.nrows * LP; i += blockDim.x) {
+    const int col = i / LP, c = (i % LP) * 4;
+    float m[WV], top = -__builtin_inff(), l = 0.f;
+#pragma unroll
+    for (int w = 0; w < WV; ++w) {
+      m[w] = ml[(w * ROWS + col) * 2];
+      top = fmaxf(top, m[w]);
+    }
+    float r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < WV; ++w) {
+      const float a = part_weight(m[w], top);
+      const float* from = o + (w * ROWS + col) * (D + 4) + c;
+      l += a * ml[(w * ROWS + col) * 2 + 1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] += a * from[e];
+    }
+    if (whole) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] *= inv;
+      const int64_t row = out_row(p, u, h, u.row0 + col);
+      storev<T, 4>(static_cast<T*>(p.o) + row * D + c, r);
+      if (p.lse && c == 0) p.lse[row] = row_lse(top, l);
+    } else {
+      storev<float, 4>(part + (int64_t)col * D + c, r);
+      if (c == 0) {
+        sums[2 * col] = top;
+        sums[2 * col + 1] = l;
+      }
+    }
+  }
+}
+
+}  // namespace gdn

@@ -1,0 +1,162 @@
+// gdn_attn_plan.hip -- how a call of the attention is cut into tiles of rows and pieces of keys, and the
+// kernel that joins the pieces.
+#include "../../include/gdn.h"
+#include "gdn_attn_device.h"
+
+namespace gdn {
+
+namespace {
+
+// Rows of units whose keys were cut, joined from their pieces: out = sum_i w_i o_i / sum_i w_i l_i with
+// w_i = 2^{m_i - max m}, in the pieces' order.  RPW rows a workgroup, 256 / RPW threads each: D / 4 columns
+// of four times groups that take every so-many-th piece.
+template <typename T, int D, int RPW>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p, int per_unit) {
+  constexpr int TEAM = 256 / RPW, LP = D / 4, GR = TEAM / LP;
+  __shared__ float acc[RPW][GR][D + 1];
+  const int lane = threadIdx.x & 63;
+  const int sub = threadIdx.x / TEAM, tid = threadIdx.x % TEAM, g = tid / LP, c = (tid % LP) * 4;
+  const int h = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk, id = rest / per_unit;
+  Unit u;
+  if (!find_unit<false>(p, id, lane, &u) || u.pieces == 1) return;
+  const int pieces = min(u.pieces, p.plan.units + p.plan.spare - u.slot);  // (fewer only with other offsets than the host's)
+  const int at = (rest - id * per_unit) * RPW + sub;
+  const bool live = at < u.nrows;
+  const int64_t step = (int64_t)p.Hk * p.plan.part_rows;  // rows from piece to piece
+  const float* part = part_outputs(p, u.slot, h) + (int64_t)at * D + c;
+  const float* ml = part_sums(p, u.slot, h) + 2 * at;
+  float top = -__builtin_inff();
+  float r[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
+  if (live) {
+    for (int i = 0; i < pieces; ++i) top = fmaxf(top, ml[2 * i * step]);
+    for (int i = g; i < pieces; i += GR) {
+      const float w = part_weight(ml[2 * i * step], top);
+      float x[4];
+      loadv<float, 4>(part + i * step * D, x);
+      l += w * ml[2 * i * step + 1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] += w * x[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[sub][g][c + e] = r[e];
+  if (c == 0) acc[sub][g][D] = l;
+  __syncthreads();
+  if (!live || g) return;
+#pragma unroll
+  for (int i = 1; i < GR; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] += acc[sub][i][c + e];
+  }
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < GR; ++i) l += acc[sub][i][D];
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] *= inv;
+  const int64_t row = out_row(p, u, h, u.row0 + at);
+  storev<T, 4>(static_cast<T*>(p.o) + row * D + c, r);
+  if (p.lse && c == 0) p.lse[row] = row_lse(top, l);
+}
+
+template <typename T, int D>
+hipError_t launch_join(const AttnParams& p, hipStream_t st) {
+  // one row a workgroup where rows are few and pieces many
+  const bool few = p.plan.part_rows <= kFewRows;
+  const int per_unit = few ? p.plan.part_rows : (p.plan.part_rows + 3) / 4;
+  const int64_t groups = (int64_t)p.plan.units * p.Hk * per_unit;
+  if (groups > kMaxGroups) return hipErrorInvalidConfiguration;
+  if (few) attn_join_kernel<T, D, 1><<<dim3((unsigned)groups), 256, 0, st>>>(p, per_unit);
+  else attn_join_kernel<T, D, 4><<<dim3((unsigned)groups), 256, 0, st>>>(p, per_unit);
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t join_width(const AttnParams& p, hipStream_t st) {
+  return p.D == 64 ? launch_join<T, 64>(p, st) : (p.D == 128 ? launch_join<T, 128>(p, st) : launch_join<T, 256>(p, st));
+}
+
+// Pieces beyond one a unit.  `fill`: workgroups that fill the chip.
+int spare_pieces(const AttnPlan& pl, int Hk, int64_t max_keys, int fill, bool always) {
+  if (!pl.units || max_keys <= pl.min_piece) return 0;
+  const int64_t have = (int64_t)pl.units * Hk;
+  int64_t want = have < fill ? fill - have : 0;
+  if (always && want < fill / 2) want = fill / 2;
+  const int64_t spare = (want + Hk - 1) / Hk;
+  return (int)spare;
+}
+
+}  // namespace
+
+AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtype, int64_t max_keys) {
+  AttnPlans a{};
+  const bool f32 = dtype == GDN_DTYPE_F32;
+  const int64_t few_limit = f32 ? INT64_MAX : kFewRows;
+  const int many = many_rows(D);
+  int64_t most_few = 0, units_many = 0, most_many = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t rows = (int64_t)(cu ? cu[i + 1] - cu[i] : T) * G;
+    if (rows <= few_limit) {
+      if (rows > most_few) most_few = rows;
+    } else {
+      units_many += (rows + many - 1) / many;
+      if (rows > most_many) most_many = rows;
+    }
+    if (!cu) {
+      units_many *= n;
+      break;
+    }
+  }
+  // 32-row tiles of 256 columns would not fit into registers
+  a.few.rows = most_few <= 16 || D == 256 ? 16 : 32;
+  int64_t units_few = 0;
+  if (most_few) {
+    for (int i = 0; i < n; ++i) {
+      const int64_t rows = (int64_t)(cu ? cu[i + 1] - cu[i] : T) * G;
+      if (rows <= few_limit) units_few += (rows + a.few.rows - 1) / a.few.rows;
+      if (!cu) {
+        units_few *= n;
+        break;
+      }
+    }
+  }
+  const int64_t most = INT32_MAX / 2;
+  a.few.units = (int)(units_few < most ? units_few : most);
+  a.few.part_rows = (int)(most_few < a.few.rows ? most_few : a.few.rows);
+  a.few.min_piece = 256;
+  a.few.spare = spare_pieces(a.few, Hk, max_keys, 1024, true);
+  a.many.rows = many;
+  a.many.units = (int)(units_many < most ? units_many : most);
+  a.many.part_rows = (int)(most_many < many ? most_many : many);
+  a.many.min_piece = 512;
+  a.many.spare = spare_pieces(a.many, Hk, max_keys, 384, false);
+  return a;
+}
+
+static size_t part_bytes(const AttnPlan& pl, int Hk, int D) {
+  if (!pl.units || !pl.spare) return 0;
+  const size_t n = ((size_t)pl.units + pl.spare) * Hk * pl.part_rows * (D + 2) * sizeof(float);
+  return (n + 255) & ~size_t{255};
+}
+size_t attn_ws_bytes(const AttnPlans& pl, int Hk, int D) { return part_bytes(pl.few, Hk, D) + part_bytes(pl.many, Hk, D); }
+
+hipError_t launch_attn_join(const AttnParams& p, int dtype, hipStream_t st) {
+  return dtype == GDN_DTYPE_BF16 ? join_width<bf16>(p, st) : join_width<float>(p, st);
+}
+
+hipError_t launch_attn(AttnParams p, const AttnPlans& pl, int dtype, bool q8, void* ws, hipStream_t st) {
+  char* at = static_cast<char*>(ws);
+  for (int many = 1; many >= 0; --many) {  // the class with more work goes first
+    p.plan = many ? pl.many : pl.few;
+    if (!p.plan.units) continue;
+    p.cls = dtype == GDN_DTYPE_F32 || !(many ? pl.few : pl.many).units ? kAllRows : (many ? kMany : kFew);
+    p.part = reinterpret_cast<float*>(at);
+    at += part_bytes(p.plan, p.Hk, p.D);
+    hipError_t e = dtype == GDN_DTYPE_F32 ? launch_attn_f32(p, q8, st)
+                                          : (many ? launch_attn_many(p, q8, st) : launch_attn_few(p, q8, st));
+    if (e == hipSuccess && p.plan.spare) e = launch_attn_join(p, dtype, st);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace gdn

@@ -29,7 +29,11 @@
  *  - the layer operators around a recurrent scan, each with its gradient and its single-token
  *    form where it has one: the short causal convolution (causal_conv_*), the selective state
  *    space scan (ssm_scan_*, ssm_step) and the residual RMS norm with an 8-bit output
- *    (rms_norm_*).
+ *    (rms_norm_*);
+ *  - the operators of the full-attention layers that stand between recurrent ones: rotary
+ *    positions and their gradient (rope_*), the paged cache of keys and values, 8-bit or not
+ *    (kv_cache_*), and the attention of new tokens over it, for chunks and for single tokens
+ *    (paged_attn_*).
  *
  * Conventions shared by every entry point.
  *  - All tensor pointers are DEVICE pointers unless the name ends in _host.  The caller owns
@@ -85,6 +89,7 @@ extern "C" {
 
 #define GDN_DTYPE_F32 0
 #define GDN_DTYPE_BF16 1
+#define GDN_DTYPE_E4M3 2 /* of a cache only: OCP e4m3 (no infinity, largest 448) with scales */
 
 /* Flags of the forward workspace queries: what the call they size will ask for. */
 #define GDN_FWD_PER_KEY 1u /* gk is given                                */
@@ -821,6 +826,102 @@ GDN_API int rms_norm_bwd(const void* dy, int64_t dy_pitch, const void* s, int64_
                          const float* w, const float* rstd, const void* dsum, int64_t dsum_pitch,
                          void* ds, void* dx, float* dw, int M, int D, int dtype, int sdtype,
                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Full-attention layers.  Conventions beside the shared ones:
+ *  - head tensors x [tokens, H, D] have a pitch (elements from token to token) and a head pitch
+ *    (from head to head), at least D and at most 2^32 each, so that columns of a projection's output
+ *    and heads-first layouts are read in place.  Outputs are dense.  A call has at most GDN_MAX_TOKENS
+ *    tokens; calls beyond a launch's threads are GDN_ERR_INVALID.
+ *  - a cache is k_cache, v_cache [pages, Hk, P, D] of the activations' dtype, or of GDN_DTYPE_E4M3 with
+ *    k_scale, v_scale [pages, Hk, P] fp32 (NULL otherwise): a row stands for its values times its scale.  P, the
+ *    places of a page, is 16, 32, .. or 1024 (GDN_ERR_UNSUPPORTED otherwise); pages * P < 2^31.
+ *  - scores, softmax statistics and sums are fp32, each result is rounded once; with bf16 activations the
+ *    softmax's weights enter the product with the values as bf16.  Results are deterministic.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * rope_fwd -- rotary positions.  Pair i (0 <= i < R / 2) of a head's first R columns, (u, w) = columns
+ * (2 i, 2 i + 1) if interleaved, else (i, i + R / 2), is turned by a = 2 pi fraction(position * turns_i):
+ *     (u, w) <- magnitude (u cos a - w sin a, u sin a + w cos a);   columns R .. D - 1 pass
+ *   x [T, H, D] dtype;  positions [T] int32 (any value);  y [T, H, D] dtype OUT
+ *   table [R / 2] uint64: turns_i in 2^-64 turns a position, so angles are exact to 2^-32 turns at any
+ *   position
+ * Supported: D <= 1024, even R in 2 .. D.
+ */
+GDN_API int rope_fwd(const void* x, int64_t x_pitch, int64_t x_head_pitch, const int* positions,
+                     const uint64_t* table, float magnitude, void* y, int T, int H, int D, int R,
+                     int interleaved, int dtype, void* stream);
+/* Its gradient: dy turned backwards and scaled by magnitude. */
+GDN_API int rope_bwd(const void* dy, int64_t dy_pitch, int64_t dy_head_pitch, const int* positions,
+                     const uint64_t* table, float magnitude, void* dx, int T, int H, int D, int R,
+                     int interleaved, int dtype, void* stream);
+
+/*
+ * kv_cache_write -- rows of keys and values into their places of a cache.
+ *   k, v [T, H, D] dtype;  slots [T] int32 (device): place slot % P of page slot / P.  A row whose slot is outside
+ *   [0, pages * P) (a padded row) changes nothing, nor does a row that names the slot of an earlier
+ *   row: the first row of a slot is the one that counts.
+ *   e4m3: scale = max(max |x|, 1e-12) / 448 over a token and head's D columns, values e4m3(x / scale) to
+ *   nearest even.  A NaN makes its row's scale and values NaN.
+ * Supported: D <= 512, H <= 4096.
+ */
+GDN_API int kv_cache_write(const void* k, int64_t k_pitch, int64_t k_head_pitch, const void* v,
+                           int64_t v_pitch, int64_t v_head_pitch, const int* slots, void* k_cache,
+                           void* v_cache, float* k_scale, float* v_scale, int T, int pages, int P,
+                           int H, int D, int dtype, int cache_dtype, void* stream);
+/* The rows at slots, read back: k, v [T, H, D] dtype OUT, 0 where a slot is outside the cache. */
+GDN_API int kv_cache_read(const void* k_cache, const void* v_cache, const float* k_scale,
+                          const float* v_scale, const int* slots, void* k, void* v, int T, int pages,
+                          int P, int H, int D, int dtype, int cache_dtype, void* stream);
+
+/*
+ * paged_attn_fwd -- attention of B sequences' T new tokens over their cached keys and values (the new
+ * tokens' own among them: they are written first).
+ *     o = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q . k_j - m),   lse = m + log sum_j p_j
+ * over the keys j that a token sees: with causal, token t is at position seq_len - T + t and sees the
+ * positions up to its own (with window > 0 the last `window` of them, its own included); otherwise it sees all
+ * seq_len keys (cross attention to cached states of another length).  A token that sees none gets o = 0
+ * and lse = -infinity.  What lies in places that a token does not see does not matter, infinities and NaN
+ * included.
+ *   q [B, T, Hq, D] dtype (tokens evenly spaced);  query heads h * Hq / Hk .. share key head h
+ *   block_table [B, max_pages] int32 (rows table_pitch apart): page of a sequence's places 0 .. P - 1,
+ *   P .. 2 P - 1, ..; entries behind its length are not read.  A page outside [0, pages) reads as keys and
+ *   values of 0.
+ *   seq_lens [B] int32 (device): keys of each sequence; taken as the nearest number in [0, max_pages * P]
+ *   o [B, T, Hq, D] dtype OUT;  lse [B, T, Hq] fp32 OUT or NULL
+ *   workspace  at least paged_attn_workspace_bytes (0 where no keys are cut), 256-byte aligned
+ * k_cache, v_cache and o must be 16-byte aligned.  How a call is cut into pieces of keys follows from its
+ * sizes and seq_lens; results of another cut differ in fp32 rounding only.
+ * Supported: D 64, 128 or 256; Hq a multiple of Hk; scale > 0.
+ */
+GDN_API size_t paged_attn_workspace_bytes(int B, int T, int Hq, int Hk, int D, int P, int max_pages,
+                                          int dtype);
+GDN_API int paged_attn_fwd(const void* q, int64_t q_pitch, int64_t q_head_pitch, const void* k_cache,
+                           const void* v_cache, const float* k_scale, const float* v_scale,
+                           const int* block_table, int64_t table_pitch, int max_pages,
+                           const int* seq_lens, float scale, int causal, int window, void* o,
+                           float* lse, int B, int T, int Hq, int Hk, int D, int pages, int P, int dtype,
+                           int cache_dtype, void* workspace, size_t workspace_bytes, void* stream);
+/* The packed form: q, o [1, T_total, Hq, D], lse [1, T_total, Hq], sequence i's new tokens in rows
+ * [cu[i], cu[i+1]); block_table [N, max_pages], seq_lens [N]. */
+GDN_API size_t paged_attn_varlen_workspace_bytes(const int* cu_seqlens_host, int N, int Hq, int Hk,
+                                                 int D, int P, int max_pages, int dtype);
+GDN_API int paged_attn_fwd_varlen(const void* q, int64_t q_pitch, int64_t q_head_pitch,
+                                  const void* k_cache, const void* v_cache, const float* k_scale,
+                                  const float* v_scale, const int* block_table, int64_t table_pitch,
+                                  int max_pages, const int* seq_lens, const int* cu_seqlens,
+                                  const int* cu_seqlens_host, int N, float scale, int causal,
+                                  int window, void* o, float* lse, int T_total, int Hq, int Hk, int D,
+                                  int pages, int P, int dtype, int cache_dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+/* One token a row, causal: q, o [B, Hq, D]; workspace as paged_attn_workspace_bytes with T = 1. */
+GDN_API int paged_attn_step(const void* q, int64_t q_pitch, int64_t q_head_pitch, const void* k_cache,
+                            const void* v_cache, const float* k_scale, const float* v_scale,
+                            const int* block_table, int64_t table_pitch, int max_pages,
+                            const int* seq_lens, float scale, int window, void* o, int B, int Hq, int Hk,
+                            int D, int pages, int P, int dtype, int cache_dtype, void* workspace,
+                            size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
