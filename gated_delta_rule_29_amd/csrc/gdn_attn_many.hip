@@ -17,17 +17,22 @@ namespace gdn {
 namespace {
 
 constexpr int kTile = 64;  // keys of a tile
+// kinds of instructions for the scheduler
+constexpr int kValu = 0x2, kMfma = 0x8, kDsRead = 0x100;
 constexpr int kRows = 32;  // of a wave
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
-typedef __attribute__((address_space(3))) u32x2v lds_u32x2;
-__device__ __forceinline__ u32x2v tr16(uint32_t lds) {
-  return __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)lds));
+typedef __attribute__((address_space(3))) char lds_char;
+__device__ __forceinline__ u32x2v tr16(lds_char* p) {
+  return __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
 }
-__device__ __forceinline__ bf16x8 read16(uint32_t lds) { return *(lds_bf16x8*)(uintptr_t)lds; }
+__device__ __forceinline__ bf16x8 read16(lds_char* p) {
+  const bf16x8 r = *(lds_bf16x8*)p;
+  return r;
+}
 __device__ __forceinline__ f32x16 mma32(const bf16x8& a, const bf16x8& b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
@@ -101,48 +106,77 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   for (int b = 0; b < DB; ++b)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[b][r] = 0.f;
-  float m = -__builtin_inff(), l = 0.f;
+  float m = -__builtin_inff(), l = 0.f;  // the maximum is of products, before the scale
 
   const uint32_t base = dma::lds_addr(lds);
   // keys: row col (and 32 more), chunk 2 s + half
-  const uint32_t kr0 = base + col * RB;
-  const int krc = half ^ swz<D>(col);
+  lds_char* kp[KS];
+#pragma unroll
+  for (int s = 0; s < KS; ++s)
+    kp[s] = (lds_char*)(uintptr_t)(base + col * RB + 16 * ((2 * s + half) ^ swz<D>(col)));
   // values, transposing: rows 4 half + (lane & 15) / 4 of each 8, columns 16 ((lane >> 4) & 1) + 4 (lane & 3)
-  const int trow = 4 * half + ((lane & 15) >> 2);
-  const uint32_t tr0 = base + M::TILE + trow * RB + 8 * (lane & 1);
-  const int trc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  lds_char* vp[2][DB];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int b = 0; b < DB; ++b) {
+      const int r = 8 * e + 4 * half + ((lane & 15) >> 2), c = 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+      vp[e][b] = (lds_char*)(uintptr_t)(base + M::TILE + r * RB + 16 * (c ^ swz<D>(r)) + 8 * (lane & 1));
+    }
 
+  // Transfers.  A wave has kTile / NW rows of a tile, which lie in one page; the page of the tile after the next
+  // is asked for with the next tile's rows.
+  constexpr int WR = NI * RPL;  // rows
+  const int nt = (u.hi - u.lo + kTile - 1) / kTile;
+  const bool carries = wv * NI < TR;
+  const __amdgpu_buffer_rsrc_t pages =
+      dma::store_rsrc(const_cast<int*>(p.table) + u.seq * p.table_pitch, (uint32_t)p.width * 4);
+  auto page_of = [&](int t) {
+    const int key = u.lo + kTile * t + wv * WR;
+    return (int)__builtin_amdgcn_raw_buffer_load_b32(pages, (key >> p.pshift) * 4 + 0 * lane, 0, 0);
+  };
+  int page_v = carries ? page_of(0) : 0;
   u32x4v kn[Q8 ? NI : 1], vn[Q8 ? NI : 1];
   float sn = 0.f;
 
-  auto ask = [&](int key, int stage) {
-    if (wv * NI < TR)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-      const int r = (wv * NI + i) * RPL;  // of the tile
-      const Window w = page_rows(p, u.seq, h, key + r, RPL, u.hi, CB);
+  auto ask = [&](int t, int stage) {
+    if (carries) {
+      const int key = u.lo + kTile * t + wv * WR, page = uni(page_v);
+      Window w{0, 0};
+      if (key < u.hi && page >= 0 && page < p.pages) {
+        w.at = (((int64_t)page * p.Hk + h) * p.P + (key & (p.P - 1))) * CB;
+        w.bytes = (uint32_t)(min(WR, u.hi - key) * CB);
+      }
       const char *kb = static_cast<const char*>(p.k) + w.at, *vb = static_cast<const char*>(p.v) + w.at;
       if constexpr (Q8) {
         const __amdgpu_buffer_rsrc_t rk = dma::store_rsrc(const_cast<char*>(kb), w.bytes);
         const __amdgpu_buffer_rsrc_t rv = dma::store_rsrc(const_cast<char*>(vb), w.bytes);
-        kn[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rk, 16 * lane, 0, 0));
-        vn[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rv, 16 * lane, 0, 0));
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          kn[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rk, 1024 * i + 16 * lane, 0, 0));
+          vn[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rv, 1024 * i + 16 * lane, 0, 0));
+        }
       } else {
-        const int x = lane / (RB / 16), c = (lane % (RB / 16)) ^ swz<D>(r + x);
-        const uint32_t at = x * RB + 16 * c;
-        const uint32_t to = uni(base + stage * M::STAGE + r * RB);
-        dma::dma16(dma::make_rsrc(kb, w.bytes), at, 0, to);
-        dma::dma16(dma::make_rsrc(vb, w.bytes), at, 0, to + M::TILE);
+        const dma::i32x4 rk = dma::make_rsrc(kb, w.bytes), rv = dma::make_rsrc(vb, w.bytes);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int r = RPL * i + lane / (RB / 16), c = (lane % (RB / 16)) ^ swz<D>(wv * WR + r);
+          const uint32_t to = uni(base + stage * M::STAGE + (wv * WR + RPL * i) * RB);
+          dma::dma16(rk, r * RB + 16 * c, 0, to);
+          dma::dma16(rv, r * RB + 16 * c, 0, to + M::TILE);
+        }
       }
+      if (t + 1 < nt) page_v = page_of(t + 1);
     }
     if constexpr (Q8) {
       // scales: the first wave the keys', the second the values'
       if (wv < 2) {
         sn = 0.f;
-        if (key + lane < u.hi) {
-          const int page = p.table[u.seq * p.table_pitch + ((key + lane) >> p.pshift)];
+        const int key = u.lo + kTile * t + lane;
+        if (key < u.hi) {
+          const int page = p.table[u.seq * p.table_pitch + (key >> p.pshift)];
           if (page >= 0 && page < p.pages)
-            sn = (wv ? p.vs : p.ks)[((int64_t)page * p.Hk + h) * p.P + ((key + lane) & (p.P - 1))];
+            sn = (wv ? p.vs : p.ks)[((int64_t)page * p.Hk + h) * p.P + (key & (p.P - 1))];
         }
       }
     }
@@ -150,39 +184,53 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   // 8-bit tiles: from registers into LDS, as bf16
   auto land = [&](int stage) {
     char* to = lds + stage * M::STAGE;
-    if (wv * NI < TR)
+    if (carries)
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-      const int r = (wv * NI + i) * RPL + lane / (D / 16), c = 2 * (lane % (D / 16)), x = swz<D>(r);
+        const int r = (wv * NI + i) * RPL + lane / (D / 16), c = 2 * (lane % (D / 16)), x = swz<D>(r);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int at = r * RB + 16 * ((c + e) ^ x);
-        *reinterpret_cast<bf16x8*>(to + at) = q8_bf16(u32x2v{kn[i][2 * e], kn[i][2 * e + 1]});
-        *reinterpret_cast<bf16x8*>(to + M::TILE + at) = q8_bf16(u32x2v{vn[i][2 * e], vn[i][2 * e + 1]});
+        for (int e = 0; e < 2; ++e) {
+          const int at = r * RB + 16 * ((c + e) ^ x);
+          *reinterpret_cast<bf16x8*>(to + at) = q8_bf16(u32x2v{kn[i][2 * e], kn[i][2 * e + 1]});
+          *reinterpret_cast<bf16x8*>(to + M::TILE + at) = q8_bf16(u32x2v{vn[i][2 * e], vn[i][2 * e + 1]});
+        }
       }
-    }
     if (wv < 2) reinterpret_cast<float*>(to + 2 * M::TILE)[wv * kTile + lane] = sn;
   };
 
-  int stage = 0;
-  if (u.lo < u.hi) ask(u.lo, 0);
-  for (int key = u.lo; key < u.hi; key += kTile, stage ^= 1) {
+  // Maxima are kept while a new one is less than 2^8 times the old one's weight: outputs and sum are then as
+  // exact, and most tiles change nothing.
+  const float slack = 8.f / p.scale;
+
+  // One tile.  EDGE: some of its keys are not seen by some of the wave's rows.
+  auto tile = [&](int t, int stage, auto edge_t) {
+    constexpr bool EDGE = decltype(edge_t)::value;
+    const int key = u.lo + kTile * t;
     if constexpr (Q8) land(stage);
     dma::wait_vm0();
     __syncthreads();  // this tile is there, and the other stage's readers are done
-    if (key + kTile < u.hi) ask(key + kTile, stage ^ 1);
-    if (key > any_last || key + kTile <= any_first) continue;  // nothing of it is seen by this wave's rows
-    const uint32_t at = stage * M::STAGE;
+    if (t + 1 < nt) ask(t + 1, stage ^ 1);
+    if constexpr (EDGE)
+      if (key > any_last || key + kTile <= any_first) return;  // nothing of it is seen by this wave's rows
+    const int at = stage * M::STAGE;
     f32x16 z[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) z[kb][r] = 0.f;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) z[kb] = mma32(read16(kr0 + at + 32 * kb * RB + 16 * (krc ^ (2 * s))), q[s], z[kb]);
+      for (int s = 0; s < KS; ++s) z[kb] = mma32(read16(kp[s] + at + 32 * kb * RB), q[s], z[kb]);
     }
-    const bool part = key + kTile - 1 > all_last || key < all_first;
-    const bool edge = part || key + kTile > u.hi;
+    if constexpr (!EDGE) {
+      // four operands ahead of the products
+      __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 0);
+#pragma unroll
+      for (int i = 0; i < 2 * KS - 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(kMfma, 4, 0);
+    }
     float top = -__builtin_inff();
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -195,7 +243,7 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
         for (int r = 0; r < 4; ++r) {
           float x = z[kb][4 * g + r];
           if constexpr (Q8) x *= ks[r];
-          if (edge) {
+          if constexpr (EDGE) {
             const int k = key + 32 * kb + 8 * g + 4 * half + r;
             x = k < u.hi && k <= last && k >= first ? x : -__builtin_inff();
           }
@@ -203,16 +251,15 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
           top = fmaxf(top, x);
         }
       }
-    // (the scale is positive: the largest product has the largest score)
-    top = max_halves(top) * p.scale;
-    if (__ballot(top > m)) {
-      const float now = fmaxf(m, top), a = part_weight(m, now);
+    top = max_halves(top);
+    if (__ballot(top > m + slack)) {
+      const float now = fmaxf(m, top), a = part_weight(m * p.scale, now * p.scale);
       m = now;
       l *= a;
 #pragma unroll
       for (int b = 0; b < DB; ++b) o[b] *= a;
     }
-    const float off = m == -__builtin_inff() ? 0.f : -m;
+    const float off = m == -__builtin_inff() ? 0.f : -m * p.scale;
     bf16x8 pf[4];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -227,29 +274,38 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
           float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x, p.scale, off));
           l += e;
           // (a hidden key's scale may be anything)
-          if constexpr (Q8) e = edge && x == -__builtin_inff() ? 0.f : e * vs[r];
+          if constexpr (Q8) e = EDGE && x == -__builtin_inff() ? 0.f : e * vs[r];
           // Weights enter the product as bf16: each is off by 2^-8 of itself at most, in either direction,
           // where the output's own rounding is as large.
           pf[2 * kb + g / 2][4 * (g & 1) + r] = (bf16)e;
         }
       }
     auto values = [&](int s, int b) {
-      const uint32_t a = tr0 + at + 16 * s * RB;
-      const u32x2v lo = tr16(a + 16 * ((4 * b) ^ trc ^ swz<D>(trow)));
-      const u32x2v hi = tr16(a + 8 * RB + 16 * ((4 * b) ^ trc ^ swz<D>(trow + 8)));
+      const u32x2v lo = tr16(vp[0][b] + at + 16 * s * RB), hi = tr16(vp[1][b] + at + 16 * s * RB);
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3));
     };
     bool odd = false;  // infinities or NaN among values that some rows do not see
-    if (part) {
+    if constexpr (EDGE) {
 #pragma unroll 1
-      for (int i = 0; i < M::TILE; i += 1024) odd |= not_finite(read16(base + at + M::TILE + i + 16 * lane));
+      for (int i = 0; i < M::TILE; i += 1024)
+        odd |= not_finite(*reinterpret_cast<const bf16x8*>(lds + at + M::TILE + i + 16 * lane));
       odd = __ballot(odd) != 0;
     }
-    if (!odd) {
+    if (!EDGE || !odd) {
 #pragma unroll
       for (int s = 0; s < 4; ++s)
 #pragma unroll
         for (int b = 0; b < DB; ++b) o[b] = mma32(values(s, b), pf[s], o[b]);
+      if constexpr (!EDGE && !Q8) {
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 1);
+        __builtin_amdgcn_sched_group_barrier(kValu, 24, 1);
+#pragma unroll
+        for (int i = 0; i < 4 * DB; ++i) {
+          __builtin_amdgcn_sched_group_barrier(kMfma, 1, 1);
+          __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 1);
+          __builtin_amdgcn_sched_group_barrier(kValu, 24 / DB, 1);
+        }
+      }
     } else {
       // a product with a weight of 0 would not be 0: such values are added where they are seen, and taken out
 #pragma unroll
@@ -258,10 +314,10 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
         for (int j = 0; j < kTile; ++j) {
           const int k = key + j;
           const bool seen = k < u.hi && k <= last && k >= first;
-          const uint32_t from = base + at + M::TILE + j * RB + 8 * half;
+          const char* from = lds + at + M::TILE + j * RB + 8 * half;
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const u32x2v w = *(lds_u32x2*)(uintptr_t)(from + 16 * ((4 * b + g) ^ swz<D>(j)));
+            const u32x2v w = *reinterpret_cast<const u32x2v*>(from + 16 * ((4 * b + g) ^ swz<D>(j)));
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float x = __uint_as_float(r & 1 ? w[r / 2] & 0xffff0000u : w[r / 2] << 16);
@@ -279,7 +335,32 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
           __builtin_amdgcn_sched_barrier(0);
         }
     }
+  };
+
+  // Tiles [in0, in1) are seen whole by all of the wave's rows; the others, first and last, are masked.
+  int in0 = nt, in1 = nt;
+  if (r1 >= r0) {
+    in0 = min(nt, max(0, all_first - u.lo + kTile - 1) / kTile);
+    in1 = min(nt, max(0, min(all_last + 1, u.hi) - u.lo) / kTile);
+    in0 = (in0 + 1) & ~1;  // (two at a time, in their stages)
+    if (in1 - in0 < 2) in0 = in1 = nt;
   }
+  if (nt) {
+    dma::wait_vm0();
+    ask(0, 0);
+  }
+  int t = 0;
+  for (int end = in0;; end = nt) {
+#pragma unroll 1
+    for (; t < end; ++t) tile(t, t & 1, std::true_type{});
+    if (t >= nt) break;
+#pragma unroll 1
+    for (; t + 2 <= in1; t += 2) {
+      tile(t, 0, std::false_type{});
+      tile(t + 1, 1, std::false_type{});
+    }
+  }
+  m *= p.scale;
 
   l = add_halves(l);
   if (!live) return;
