@@ -50,7 +50,7 @@ hipError_t launch_cache_read(const CacheRowsParams& p, int dtype, bool q8, hipSt
 struct AttnPlan {
   int rows;        // of a tile
   int units;       // tiles of all sequences of the class
-  int spare;       // pieces beyond one a unit (0: no unit is cut)
+  int spare;       // pieces beyond one a unit, at most (0: no unit is cut; cut units have 2 * spare at most)
   int min_piece;   // keys
   int part_rows;   // rows of a tile that exist (the pitch of partial results)
 };
@@ -78,7 +78,7 @@ struct AttnParams {
   int window;               // 0: none
   int cls;
   AttnPlan plan;
-  float* part;              // workspace: outputs [pieces][Hk][part_rows][D], then maxima and sums [..][2]
+  float* part;              // workspace: outputs [2 * spare][Hk][part_rows][D], then maxima and sums [..][2]
 };
 
 struct AttnPlans {

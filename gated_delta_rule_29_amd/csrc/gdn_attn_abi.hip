@@ -155,7 +155,7 @@ int attn(const gdn::Seqs& s, const int* cu_host, const Attn& a, void* ws, size_t
   // (512 threads a workgroup at most)
   for (const gdn::AttnPlan& q : {pl.few, pl.many})
     if (((int64_t)q.units + q.spare) * a.Hk > gdn::kMaxGroups / 2 ||
-        (q.spare && (int64_t)q.units * a.Hk * q.part_rows > gdn::kMaxGroups))
+        (int64_t)q.spare * a.Hk * q.part_rows > gdn::kMaxGroups)
       return fail(GDN_ERR_INVALID, "%s of these sizes exceeds the grid limit", what);
   GDN_TRY(check_workspace(ws, ws_bytes, gdn::attn_ws_bytes(pl, a.Hk, a.D)));
   gdn::AttnParams p{};

@@ -12,7 +12,7 @@ namespace gdn {
 struct Unit {
   int seq, tile;        // tile: row0 / rows of a tile
   int piece, pieces;    // of the unit
-  int slot;             // number of the piece among all pieces (of a unit's first piece: with piece 0)
+  int slot;             // number of the piece among the pieces of all cut units
   int begin, n;         // the sequence's first row in the batch and its tokens
   int len;              // its keys
   int row0, nrows;      // the unit's rows
@@ -39,8 +39,8 @@ __device__ __forceinline__ int attn_span(const AttnParams& p, int len) {
 
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// Pieces have this many keys at least: so many that the units are cut into `spare` pieces more than there are
-// units.  Every wave of every workgroup finds the same number, by itself.
+// Keys of a piece, about: so many that the units are cut into at most `spare` pieces more than there are units (a
+// unit of n keys into n / keys, rounded: sum of tiles * (pieces - 1) <= sum of tiles * span / keys).  Every wave of every workgroup finds the same number, by itself.
 __device__ __forceinline__ int attn_piece_keys(const AttnParams& p, int lane) {
   if (p.plan.spare == 0) return 0x7fffffc0;
   int64_t sum = 0;
@@ -54,55 +54,58 @@ __device__ __forceinline__ int attn_piece_keys(const AttnParams& p, int lane) {
   return uni((int)min((keys + 63) & ~int64_t{63}, int64_t{0x7fffffc0}));
 }
 
-// Finds piece number `id` (PIECES) or the first piece of unit number `id`; false beyond the last one.
+// Pieces of n keys.
+__device__ __forceinline__ int attn_pieces(int n, int keys) { return max(1, (int)(((int64_t)n + keys / 2) / keys)); }
+
+// Finds piece number `id` (PIECES), or the first piece of unit number `id` of those that may be cut; false where
+// there is nothing to do.
 template <bool PIECES>
 __device__ __forceinline__ bool find_unit(const AttnParams& p, int id, int lane, Unit* u) {
   const int keys = attn_piece_keys(p, lane);
-  int before_t = 0, before_p = 0;  // tiles and pieces of the sequences looked at
-  int seq = -1, tiles_at = 0, pieces_at = 0, per_tile = 1;
+  int before = 0, before_cut = 0;  // what is counted, and cut units' pieces, of the sequences looked at
+  int seq = -1, at = 0, cut_at = 0, per_tile = 1;
   if (p.plan.spare == 0 && !p.s.cu) {  // sequences alike
     const int tiles = (p.s.T * p.G + p.plan.rows - 1) / p.plan.rows;
     seq = id / tiles;
     if (seq >= p.s.n) return false;
-    tiles_at = pieces_at = seq * tiles;
+    at = seq * tiles;
   } else {
     for (int base = 0; base < p.s.n && seq < 0; base += 64) {
       const int i = base + lane;
       int tiles = 0, k = 1;
       if (i < p.s.n) {
         tiles = attn_tiles(p, attn_tokens(p, i) * p.G);
-        if (p.plan.spare) k = max(1, (attn_span(p, attn_len(p, i)) + keys - 1) / keys);
+        if (p.plan.spare) k = attn_pieces(attn_span(p, attn_len(p, i)), keys);
       }
-      int it = tiles, ip = tiles * k;
+      const int cut = k > 1 ? tiles * k : 0, mine = PIECES ? tiles * k : (k > 1 ? tiles : 0);
+      int sum = mine, sum_cut = cut;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
-        const int a = __shfl_up(it, off, 64), b = __shfl_up(ip, off, 64);
+        const int a = __shfl_up(sum, off, 64), b = __shfl_up(sum_cut, off, 64);
         if (lane >= off) {
-          it += a;
-          ip += b;
+          sum += a;
+          sum_cut += b;
         }
       }
-      const int here = PIECES ? ip : it, mine = PIECES ? tiles * k : tiles, before = PIECES ? before_p : before_t;
-      const unsigned long long m = __ballot(id < before + here && id >= before + here - mine);
+      const unsigned long long m = __ballot(id < before + sum && id >= before + sum - mine);
       if (m) {
         const int l = __builtin_ctzll(m);
         seq = base + l;
         per_tile = uni(__shfl(k, l, 64));
-        tiles_at = before_t + uni(__shfl(it - tiles, l, 64));
-        pieces_at = before_p + uni(__shfl(ip - tiles * k, l, 64));
+        at = before + uni(__shfl(sum - mine, l, 64));
+        cut_at = before_cut + uni(__shfl(sum_cut - cut, l, 64));
       }
-      before_t += uni(__shfl(it, 63, 64));
-      before_p += uni(__shfl(ip, 63, 64));
+      before += uni(__shfl(sum, 63, 64));
+      before_cut += uni(__shfl(sum_cut, 63, 64));
     }
     if (seq < 0) return false;
   }
   seq = uni(seq);
-  const int off = PIECES ? id - pieces_at : (id - tiles_at) * per_tile;
+  const int off = PIECES ? id - at : (id - at) * per_tile;
   u->seq = seq;
-  u->pieces = per_tile;
   u->tile = off / per_tile;
   u->piece = off - u->tile * per_tile;
-  u->slot = pieces_at + off;
+  u->slot = cut_at + off;
   u->begin = uni(seq_begin(p.s, seq));
   u->n = uni(attn_tokens(p, seq));
   u->len = uni(attn_len(p, seq));
@@ -114,7 +117,10 @@ __device__ __forceinline__ bool find_unit(const AttnParams& p, int id, int lane,
     end = max(0, min(end, u->len - u->n + (u->row0 + u->nrows - 1) / p.G + 1));
     if (p.window) base = min(end, max(0, u->len - u->n + u->row0 / p.G - p.window + 1)) & ~63;
   }
-  const int share = ((end - base + per_tile - 1) / per_tile + 63) & ~63;
+  // (a causal sequence's first tiles see fewer keys than its last one, and may have fewer pieces)
+  u->pieces = p.plan.spare ? min(per_tile, attn_pieces(end - base, keys)) : 1;
+  if (PIECES ? u->piece >= u->pieces : u->pieces == 1) return false;
+  const int share = ((end - base + u->pieces - 1) / u->pieces + 63) & ~63;
   const int64_t lo = base + (int64_t)u->piece * share;
   u->lo = (int)min(lo, (int64_t)end);
   u->hi = (int)min(lo + share, (int64_t)end);
@@ -192,7 +198,7 @@ __device__ __forceinline__ float* part_outputs(const AttnParams& p, int slot, in
   return p.part + ((int64_t)slot * p.Hk + h) * p.plan.part_rows * p.D;
 }
 __device__ __forceinline__ float* part_sums(const AttnParams& p, int slot, int h) {
-  const int64_t before = (int64_t)(p.plan.units + p.plan.spare) * p.Hk * p.plan.part_rows * p.D;
+  const int64_t before = 2 * (int64_t)p.plan.spare * p.Hk * p.plan.part_rows * p.D;
   return p.part + before + ((int64_t)slot * p.Hk + h) * p.plan.part_rows * 2;
 }
 

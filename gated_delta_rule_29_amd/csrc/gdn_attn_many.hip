@@ -68,9 +68,8 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   __shared__ __attribute__((aligned(1024))) char lds[M::LDS];
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), col = lane & 31, half = lane >> 5;
   const int h = blockIdx.x % p.Hk;
-  int id = blockIdx.x / p.Hk;
-  // uncut units in descending order: a causal sequence's last rows see the most keys
-  if (p.plan.spare == 0) id = p.plan.units - 1 - id;
+  // descending: a causal sequence's last rows see the most keys
+  const int id = p.plan.units + p.plan.spare - 1 - blockIdx.x / p.Hk;
   Unit u;
   if (!find_unit<true>(p, id, lane, &u)) return;
 

@@ -8,66 +8,81 @@ namespace gdn {
 namespace {
 
 // Rows of units whose keys were cut, joined from their pieces: out = sum_i w_i o_i / sum_i w_i l_i with
-// w_i = 2^{m_i - max m}, in the pieces' order.  RPW rows a workgroup, 256 / RPW threads each: D / 4 columns
-// of four times groups that take every so-many-th piece.
+// w_i = 2^{m_i - max m}, with a running maximum.  RPW rows at a time, 256 / RPW threads each: D / 4 columns of
+// four times groups that take every so-many-th piece, joined in LDS in a fixed order.  A workgroup takes `rows`
+// rows of a unit: most workgroups of a call that cuts little find nothing to do, so they are few.
 template <typename T, int D, int RPW>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p, int per_unit) {
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p, int per_unit, int rows) {
   constexpr int TEAM = 256 / RPW, LP = D / 4, GR = TEAM / LP;
-  __shared__ float acc[RPW][GR][D + 1];
+  __shared__ float acc[RPW][GR][D + 2];
   const int lane = threadIdx.x & 63;
   const int sub = threadIdx.x / TEAM, tid = threadIdx.x % TEAM, g = tid / LP, c = (tid % LP) * 4;
   const int h = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk, id = rest / per_unit;
   Unit u;
-  if (!find_unit<false>(p, id, lane, &u) || u.pieces == 1) return;
-  const int pieces = min(u.pieces, p.plan.units + p.plan.spare - u.slot);  // (fewer only with other offsets than the host's)
-  const int at = (rest - id * per_unit) * RPW + sub;
-  const bool live = at < u.nrows;
+  if (!find_unit<false>(p, id, lane, &u)) return;
+  const int pieces = min(u.pieces, 2 * p.plan.spare - u.slot);  // (fewer only with other offsets than the host's)
   const int64_t step = (int64_t)p.Hk * p.plan.part_rows;  // rows from piece to piece
-  const float* part = part_outputs(p, u.slot, h) + (int64_t)at * D + c;
-  const float* ml = part_sums(p, u.slot, h) + 2 * at;
-  float top = -__builtin_inff();
-  float r[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-  if (live) {
-    for (int i = 0; i < pieces; ++i) top = fmaxf(top, ml[2 * i * step]);
-    for (int i = g; i < pieces; i += GR) {
-      const float w = part_weight(ml[2 * i * step], top);
-      float x[4];
-      loadv<float, 4>(part + i * step * D, x);
-      l += w * ml[2 * i * step + 1];
+  const int first = (rest - id * per_unit) * rows, end = min(first + rows, u.nrows);
+  for (int at0 = first; at0 < end; at0 += RPW) {
+    const int at = at0 + sub;
+    const float* part = part_outputs(p, u.slot, h) + (int64_t)at * D + c;
+    const float* ml = part_sums(p, u.slot, h) + 2 * at;
+    float top = -__builtin_inff(), l = 0.f;
+    float r[4] = {0.f, 0.f, 0.f, 0.f};
+    if (at < end) {
+#pragma unroll 4
+      for (int i = g; i < pieces; i += GR) {
+        float x[4], s[2];
+        loadv<float, 4>(part + i * step * D, x);
+        loadv<float, 2>(ml + 2 * i * step, s);
+        const float now = fmaxf(top, s[0]), a = part_weight(top, now), w = part_weight(s[0], now);
+        top = now;
+        l = l * a + w * s[1];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] += w * x[e];
+        for (int e = 0; e < 4; ++e) r[e] = r[e] * a + w * x[e];
+      }
     }
+    __syncthreads();  // the last rows' readers are done
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[sub][g][c + e] = r[e];
+    if (c == 0) {
+      acc[sub][g][D] = top;
+      acc[sub][g][D + 1] = l;
+    }
+    __syncthreads();
+    if (at >= end || g) continue;
+    float all = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < GR; ++i) all = fmaxf(all, acc[sub][i][D]);
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < GR; ++i) {
+      const float w = part_weight(acc[sub][i][D], all);
+      l += w * acc[sub][i][D + 1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] += w * acc[sub][i][c + e];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] *= inv;
+    const int64_t row = out_row(p, u, h, u.row0 + at);
+    storev<T, 4>(static_cast<T*>(p.o) + row * D + c, r);
+    if (p.lse && c == 0) p.lse[row] = row_lse(all, l);
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) acc[sub][g][c + e] = r[e];
-  if (c == 0) acc[sub][g][D] = l;
-  __syncthreads();
-  if (!live || g) return;
-#pragma unroll
-  for (int i = 1; i < GR; ++i) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] += acc[sub][i][c + e];
-  }
-  l = 0.f;
-#pragma unroll
-  for (int i = 0; i < GR; ++i) l += acc[sub][i][D];
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) r[e] *= inv;
-  const int64_t row = out_row(p, u, h, u.row0 + at);
-  storev<T, 4>(static_cast<T*>(p.o) + row * D + c, r);
-  if (p.lse && c == 0) p.lse[row] = row_lse(top, l);
 }
 
 template <typename T, int D>
 hipError_t launch_join(const AttnParams& p, hipStream_t st) {
   // one row a workgroup where rows are few and pieces many
   const bool few = p.plan.part_rows <= kFewRows;
-  const int per_unit = few ? p.plan.part_rows : (p.plan.part_rows + 3) / 4;
-  const int64_t groups = (int64_t)p.plan.units * p.Hk * per_unit;
+  const int rows = few ? 1 : 32, per_unit = (p.plan.part_rows + rows - 1) / rows;
+  // (there are at most `spare` cut units)
+  const int64_t groups = (int64_t)(p.plan.units < p.plan.spare ? p.plan.units : p.plan.spare) * p.Hk * per_unit;
   if (groups > kMaxGroups) return hipErrorInvalidConfiguration;
-  if (few) attn_join_kernel<T, D, 1><<<dim3((unsigned)groups), 256, 0, st>>>(p, per_unit);
-  else attn_join_kernel<T, D, 4><<<dim3((unsigned)groups), 256, 0, st>>>(p, per_unit);
+  if (few) attn_join_kernel<T, D, 1><<<dim3((unsigned)groups), 256, 0, st>>>(p, per_unit, rows);
+  else attn_join_kernel<T, D, 4><<<dim3((unsigned)groups), 256, 0, st>>>(p, per_unit, rows);
   return hipGetLastError();
 }
 template <typename T>
@@ -75,14 +90,16 @@ hipError_t join_width(const AttnParams& p, hipStream_t st) {
   return p.D == 64 ? launch_join<T, 64>(p, st) : (p.D == 128 ? launch_join<T, 128>(p, st) : launch_join<T, 256>(p, st));
 }
 
-// Pieces beyond one a unit.  `fill`: workgroups that fill the chip.
-int spare_pieces(const AttnPlan& pl, int Hk, int64_t max_keys, int fill, bool always) {
-  if (!pl.units || max_keys <= pl.min_piece) return 0;
+// Pieces beyond one a unit: as many as fill the chip (`fill` workgroups) where the units do not, and half of
+// that in any case, so that a sequence much longer than the others is cut.  least: tiles of the sequence that
+// has the fewest; if they are as many as the pieces, no sequence is long enough among the others to be cut.
+int spare_pieces(const AttnPlan& pl, int Hk, int64_t max_keys, int fill, int64_t least) {
+  if (!pl.units || 2 * max_keys < 3 * pl.min_piece) return 0;
   const int64_t have = (int64_t)pl.units * Hk;
   int64_t want = have < fill ? fill - have : 0;
-  if (always && want < fill / 2) want = fill / 2;
+  if (want < fill / 2) want = fill / 2;
   const int64_t spare = (want + Hk - 1) / Hk;
-  return (int)spare;
+  return least >= spare ? 0 : (int)spare;
 }
 
 }  // namespace
@@ -92,49 +109,47 @@ AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtyp
   const bool f32 = dtype == GDN_DTYPE_F32;
   const int64_t few_limit = f32 ? INT64_MAX : kFewRows;
   const int many = many_rows(D);
-  int64_t most_few = 0, units_many = 0, most_many = 0;
-  for (int i = 0; i < n; ++i) {
-    const int64_t rows = (int64_t)(cu ? cu[i + 1] - cu[i] : T) * G;
+  // (a dense batch's sequences are alike: the first stands for all)
+  const int seqs = cu ? n : 1, times = cu ? 1 : n;
+  const auto rows_of = [&](int i) { return (int64_t)(cu ? cu[i + 1] - cu[i] : T) * G; };
+  int64_t most_few = 0, units_many = 0, most_many = 0, least_many = INT64_MAX;
+  for (int i = 0; i < seqs; ++i) {
+    const int64_t rows = rows_of(i);
     if (rows <= few_limit) {
       if (rows > most_few) most_few = rows;
     } else {
-      units_many += (rows + many - 1) / many;
+      const int64_t tiles = (rows + many - 1) / many;
+      units_many += tiles * times;
       if (rows > most_many) most_many = rows;
-    }
-    if (!cu) {
-      units_many *= n;
-      break;
+      if (tiles < least_many) least_many = tiles;
     }
   }
   // 32-row tiles of 256 columns would not fit into registers
   a.few.rows = most_few <= 16 || D == 256 ? 16 : 32;
-  int64_t units_few = 0;
-  if (most_few) {
-    for (int i = 0; i < n; ++i) {
-      const int64_t rows = (int64_t)(cu ? cu[i + 1] - cu[i] : T) * G;
-      if (rows <= few_limit) units_few += (rows + a.few.rows - 1) / a.few.rows;
-      if (!cu) {
-        units_few *= n;
-        break;
-      }
-    }
+  int64_t units_few = 0, least_few = INT64_MAX;
+  for (int i = 0; most_few && i < seqs; ++i) {
+    const int64_t rows = rows_of(i);
+    if (rows > few_limit) continue;
+    const int64_t tiles = (rows + a.few.rows - 1) / a.few.rows;
+    units_few += tiles * times;
+    if (tiles < least_few) least_few = tiles;
   }
   const int64_t most = INT32_MAX / 2;
   a.few.units = (int)(units_few < most ? units_few : most);
   a.few.part_rows = (int)(most_few < a.few.rows ? most_few : a.few.rows);
-  a.few.min_piece = 256;
-  a.few.spare = spare_pieces(a.few, Hk, max_keys, 1024, true);
+  a.few.min_piece = 512;
+  a.few.spare = spare_pieces(a.few, Hk, max_keys, 1024, least_few);
   a.many.rows = many;
   a.many.units = (int)(units_many < most ? units_many : most);
   a.many.part_rows = (int)(most_many < many ? most_many : many);
-  a.many.min_piece = 512;
-  a.many.spare = spare_pieces(a.many, Hk, max_keys, 384, false);
+  a.many.min_piece = 1024;
+  a.many.spare = spare_pieces(a.many, Hk, max_keys, 512, least_many);
   return a;
 }
 
 static size_t part_bytes(const AttnPlan& pl, int Hk, int D) {
   if (!pl.units || !pl.spare) return 0;
-  const size_t n = ((size_t)pl.units + pl.spare) * Hk * pl.part_rows * (D + 2) * sizeof(float);
+  const size_t n = 2 * (size_t)pl.spare * Hk * pl.part_rows * (D + 2) * sizeof(float);
   return (n + 255) & ~size_t{255};
 }
 size_t attn_ws_bytes(const AttnPlans& pl, int Hk, int D) { return part_bytes(pl.few, Hk, D) + part_bytes(pl.many, Hk, D); }
