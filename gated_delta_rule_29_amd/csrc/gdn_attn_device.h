@@ -135,21 +135,18 @@ __device__ __forceinline__ int first_key(const AttnParams& p, int last) {
   return p.window ? max(0, last - p.window + 1) : 0;  // (an empty row's last key is negative)
 }
 
-// A cache's rows [key, key + rows) of a head, which lie in one page, as a bounds-checked window: rows at or
+// A cache's rows [key, key + rows) of a head, which lie in this page, as a bounds-checked window: rows at or
 // behind `end`, and pages that the cache does not have, read as zeros.  `row`: bytes.
 struct Window {
   int64_t at;      // byte offset in the cache
   uint32_t bytes;
 };
-__device__ __forceinline__ Window page_rows(const AttnParams& p, int seq, int h, int key, int rows, int end,
+__device__ __forceinline__ Window page_rows(const AttnParams& p, int page, int h, int key, int rows, int end,
                                             int row) {
   Window w{0, 0};
-  if (key < end) {
-    const int page = p.table[seq * p.table_pitch + (key >> p.pshift)];
-    if (page >= 0 && page < p.pages) {
-      w.at = (((int64_t)page * p.Hk + h) * p.P + (key & (p.P - 1))) * row;
-      w.bytes = (uint32_t)(min(rows, end - key) * row);
-    }
+  if (key < end && page >= 0 && page < p.pages) {
+    w.at = (((int64_t)page * p.Hk + h) * p.P + (key & (p.P - 1))) * row;
+    w.bytes = (uint32_t)(min(rows, end - key) * row);
   }
   return w;
 }

@@ -54,7 +54,8 @@ __global__ __launch_bounds__(256) void attn_f32_kernel(AttnParams p) {
   }
 
   for (int key = u.lo + kTile * wv; key < u.hi; key += kTile * kWaves) {
-    const Window w = page_rows(p, u.seq, h, key, kTile, u.hi, CB);
+    const int page = p.table[u.seq * p.table_pitch + (key >> p.pshift)];
+    const Window w = page_rows(p, page, h, key, kTile, u.hi, CB);
     const __amdgpu_buffer_rsrc_t rk = dma::store_rsrc(const_cast<char*>(static_cast<const char*>(p.k)) + w.at, w.bytes);
     const __amdgpu_buffer_rsrc_t rv = dma::store_rsrc(const_cast<char*>(static_cast<const char*>(p.v)) + w.at, w.bytes);
     f32x8 k[KS];

@@ -110,11 +110,21 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnParams p) {
   f32x4 ksn[2], vsn[2];
   u32x4v vn[Q8 ? VL : 1];
 
-  // Asks for a tile's keys, values and scales.
+  // Pages of a tile's two times 16 keys (one page holds 16): asked for a tile before its keys and values.
+  const __amdgpu_buffer_rsrc_t pages =
+      dma::store_rsrc(const_cast<int*>(p.table) + u.seq * p.table_pitch, (uint32_t)p.width * 4);
+  int page_v[2];
+  auto ask_pages = [&](int key) {
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+      page_v[kt] = (int)__builtin_amdgcn_raw_buffer_load_b32(pages, ((key + 16 * kt) >> p.pshift) * 4, 0, 0);
+  };
+  // Asks for a tile's keys, values and scales, and for the next tile's pages.
   auto ask = [&](int key, int stage) {
+    const int page[2] = {uni(page_v[0]), uni(page_v[1])};
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
-      const Window w = page_rows(p, u.seq, h, key + 16 * kt, 16, u.hi, CB);
+      const Window w = page_rows(p, page[kt], h, key + 16 * kt, 16, u.hi, CB);
       const __amdgpu_buffer_rsrc_t rk = dma::store_rsrc(const_cast<char*>(static_cast<const char*>(p.k)) + w.at, w.bytes);
 #pragma unroll
       for (int s = 0; s < KL; ++s)
@@ -145,10 +155,14 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnParams p) {
         }
       }
     }
+    ask_pages(key + kTile * kWaves);
   };
 
   int key = u.lo + kTile * wv, stage = 0;
-  if (key < u.hi) ask(key, 0);
+  if (key < u.hi) {
+    ask_pages(key);
+    ask(key, 0);
+  }
   for (; key < u.hi; key += kTile * kWaves, stage ^= F::STAGES - 1) {
     dma::wait_vm0();
     u32x4v kc[2][KL];

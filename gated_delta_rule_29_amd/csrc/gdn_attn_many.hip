@@ -132,7 +132,7 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
       dma::store_rsrc(const_cast<int*>(p.table) + u.seq * p.table_pitch, (uint32_t)p.width * 4);
   auto page_of = [&](int t) {
     const int key = u.lo + kTile * t + wv * WR;
-    return (int)__builtin_amdgcn_raw_buffer_load_b32(pages, (key >> p.pshift) * 4 + 0 * lane, 0, 0);
+    return (int)__builtin_amdgcn_raw_buffer_load_b32(pages, (key >> p.pshift) * 4, 0, 0);
   };
   int page_v = carries ? page_of(0) : 0;
   u32x4v kn[Q8 ? NI : 1], vn[Q8 ? NI : 1];
@@ -141,11 +141,7 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   auto ask = [&](int t, int stage) {
     if (carries) {
       const int key = u.lo + kTile * t + wv * WR, page = uni(page_v);
-      Window w{0, 0};
-      if (key < u.hi && page >= 0 && page < p.pages) {
-        w.at = (((int64_t)page * p.Hk + h) * p.P + (key & (p.P - 1))) * CB;
-        w.bytes = (uint32_t)(min(WR, u.hi - key) * CB);
-      }
+      const Window w = page_rows(p, page, h, key, WR, u.hi, CB);
       const char *kb = static_cast<const char*>(p.k) + w.at, *vb = static_cast<const char*>(p.v) + w.at;
       if constexpr (Q8) {
         const __amdgpu_buffer_rsrc_t rk = dma::store_rsrc(const_cast<char*>(kb), w.bytes);
