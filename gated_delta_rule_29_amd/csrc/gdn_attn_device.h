@@ -164,11 +164,11 @@ __device__ __forceinline__ float max_halves(float x) {
 
 // Which of 8 bf16 values are infinite or NaN, and those values with them set to 0.
 typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
-__device__ __forceinline__ bool not_finite(const bf16x8& v) {
-  const u16x8 b = __builtin_bit_cast(u16x8, v);
-  bool r = false;
+// (an exponent of all ones carries into the sign's place when a one is added to it)
+__device__ __forceinline__ unsigned not_finite_bits(const u32x4v& v) {
+  unsigned r = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) r |= (b[i] & 0x7f80) == 0x7f80;
+  for (int i = 0; i < 4; ++i) r |= ((v[i] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
   return r;
 }
 __device__ __forceinline__ bf16x8 finite_part(const bf16x8& v) {

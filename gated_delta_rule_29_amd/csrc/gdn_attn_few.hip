@@ -261,10 +261,11 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnParams p) {
     };
     bool odd = false;  // infinities or NaN among values that some rows do not see
     if (part) {
-#pragma unroll 1
+      unsigned any = 0;
+#pragma unroll 4
       for (int i = 0; i < kTile * RB; i += 1024)
-        odd |= not_finite(*reinterpret_cast<const bf16x8*>(mine + stage * kTile * RB + i + 16 * lane));
-      odd = __ballot(odd) != 0;
+        any |= not_finite_bits(*reinterpret_cast<const u32x4v*>(mine + stage * kTile * RB + i + 16 * lane));
+      odd = __ballot(any) != 0;
     }
     if (!odd) {
 #pragma unroll

@@ -25,12 +25,11 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
-typedef __attribute__((address_space(3))) char lds_char;
-__device__ __forceinline__ u32x2v tr16(lds_char* p) {
-  return __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
+__device__ __forceinline__ u32x2v tr16(uint32_t lds) {
+  return __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)lds));
 }
-__device__ __forceinline__ bf16x8 read16(lds_char* p) {
-  const bf16x8 r = *(lds_bf16x8*)p;
+__device__ __forceinline__ bf16x8 read16(uint32_t lds) {
+  const bf16x8 r = *(lds_bf16x8*)(uintptr_t)lds;
   return r;
 }
 __device__ __forceinline__ f32x16 mma32(const bf16x8& a, const bf16x8& b, f32x16 c) {
@@ -50,18 +49,22 @@ struct Many {
   static constexpr int ROWS = kRows * NW;
   static constexpr int RB = D * 2;
   static constexpr int TILE = kTile * RB;  // bytes of a tile of keys or values in LDS
+  // Tiles that come and go together: with two, the waves meet half as often, and the two of a SIMD drift apart, so that
+  // one's products run beside the other's exponentials.
+  static constexpr int SUB = Q8 || D == 256 ? 1 : 2;
+  static constexpr int STAGE = 2 * SUB * TILE;  // keys, then values
   static constexpr int SCALES = Q8 ? 2 * kTile * 4 : 0;
-  static constexpr int STAGE = 2 * TILE + SCALES;
-  static constexpr int LDS = 2 * STAGE;
+  static constexpr int LDS = 2 * (STAGE + SCALES);
 };
 
 template <bool Q8, int D, int NW>
-__global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(AttnParams p) {
   using M = Many<Q8, D, NW>;
   constexpr int RB = M::RB, CB = Q8 ? D : 2 * D;  // bytes of a row in LDS and in the cache
   constexpr int KS = D / 16;                      // contraction steps of the scores
   constexpr int DB = D / 32;                      // blocks of output columns
-  constexpr int TR = kTile * CB / 1024;           // 1 KB transfers of a tile of keys
+  constexpr int SUB = M::SUB, KEYS = SUB * kTile; // tiles and keys of a stage
+  constexpr int TR = KEYS * CB / 1024;            // 1 KB transfers of a stage's keys
   constexpr int NI = (TR + NW - 1) / NW;          // of a wave
   static_assert(TR % NI == 0, "a wave takes NI transfers or none");
   constexpr int RPL = 1024 / CB;                  // rows of one
@@ -76,10 +79,7 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   const int row = u.row0 + kRows * wv + col;
   const bool live = row < u.row0 + u.nrows;
   const int last = last_key(p, u, row), first = first_key(p, last);
-  // of this wave's rows: keys up to all_last and from all_first on are seen by all, beyond any_last by none
-  const int r0 = u.row0 + kRows * wv, r1 = min(r0 + kRows, u.row0 + u.nrows) - 1;
-  const int all_last = uni(last_key(p, u, r0)), any_last = uni(r1 >= r0 ? last_key(p, u, r1) : -1);
-  const int all_first = uni(first_key(p, any_last)), any_first = uni(first_key(p, all_last));
+  const unsigned seen_n = (unsigned)max(0, min(last, u.hi - 1) - first + 1);  // keys of this piece from `first` on
   bf16x8 q[KS];
   {
     const int t = row / p.G;
@@ -108,71 +108,73 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   float m = -__builtin_inff(), l = 0.f;  // the maximum is of products, before the scale
 
   const uint32_t base = dma::lds_addr(lds);
+  // where a stage's operands are read; the other stage is `hop` away
+  uint32_t kp[KS], vp[2][DB];
+  int hop = M::STAGE;
   // keys: row col (and 32 more), chunk 2 s + half
-  lds_char* kp[KS];
 #pragma unroll
-  for (int s = 0; s < KS; ++s)
-    kp[s] = (lds_char*)(uintptr_t)(base + col * RB + 16 * ((2 * s + half) ^ swz<D>(col)));
+  for (int s = 0; s < KS; ++s) kp[s] = base + col * RB + 16 * ((2 * s + half) ^ swz<D>(col));
   // values, transposing: rows 4 half + (lane & 15) / 4 of each 8, columns 16 ((lane >> 4) & 1) + 4 (lane & 3)
-  lds_char* vp[2][DB];
 #pragma unroll
   for (int e = 0; e < 2; ++e)
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
       const int r = 8 * e + 4 * half + ((lane & 15) >> 2), c = 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-      vp[e][b] = (lds_char*)(uintptr_t)(base + M::TILE + r * RB + 16 * (c ^ swz<D>(r)) + 8 * (lane & 1));
+      vp[e][b] = base + SUB * M::TILE + r * RB + 16 * (c ^ swz<D>(r)) + 8 * (lane & 1);
     }
 
-  // Transfers.  A wave has kTile / NW rows of a tile, which lie in one page; the page of the tile after the next
-  // is asked for with the next tile's rows.
-  constexpr int WR = NI * RPL;  // rows
-  const int nt = (u.hi - u.lo + kTile - 1) / kTile;
+  // Transfers.  A wave has WR rows of a tile, which lie in one page; a page's number is asked for a tile ahead, as
+  // a scalar.
+  typedef __attribute__((address_space(4))) const int const_int;
+  constexpr int WR = NI * RPL;
+  const int nt = (u.hi - u.lo + kTile - 1) / kTile, ns = (nt + SUB - 1) / SUB;  // tiles and stages
   const bool carries = wv * NI < TR;
-  const __amdgpu_buffer_rsrc_t pages =
-      dma::store_rsrc(const_cast<int*>(p.table) + u.seq * p.table_pitch, (uint32_t)p.width * 4);
-  auto page_of = [&](int t) {
-    const int key = u.lo + kTile * t + wv * WR;
-    return (int)__builtin_amdgcn_raw_buffer_load_b32(pages, (key >> p.pshift) * 4, 0, 0);
-  };
-  int page_v = carries ? page_of(0) : 0;
+  const_int* table = (const_int*)(uintptr_t)(p.table + u.seq * p.table_pitch);
+  const int64_t page_bytes = (int64_t)p.Hk * p.P * CB;
+  const char *khead = static_cast<const char*>(p.k) + (int64_t)h * p.P * CB,
+             *vhead = static_cast<const char*>(p.v) + (int64_t)h * p.P * CB;
+  auto page_of = [&](int t) { return table[min(u.lo + KEYS * t + wv * WR, u.hi - 1) >> p.pshift]; };
+  int page = nt ? page_of(0) : 0;
   u32x4v kn[Q8 ? NI : 1], vn[Q8 ? NI : 1];
   float sn = 0.f;
+  auto page_of_key = [&](int t) { return p.table[u.seq * p.table_pitch + (min(u.lo + kTile * t + lane, u.hi - 1) >> p.pshift)]; };
+  int key_page = Q8 && nt && wv < 2 ? page_of_key(0) : 0;
 
   auto ask = [&](int t, int stage) {
     if (carries) {
-      const int key = u.lo + kTile * t + wv * WR, page = uni(page_v);
-      const Window w = page_rows(p, page, h, key, WR, u.hi, CB);
-      const char *kb = static_cast<const char*>(p.k) + w.at, *vb = static_cast<const char*>(p.v) + w.at;
+      const int key = u.lo + KEYS * t + wv * WR;
+      const bool there = key < u.hi && (unsigned)page < (unsigned)p.pages;
+      const int64_t from = there ? page * page_bytes + (key & (p.P - 1)) * CB : 0;
+      const uint32_t bytes = there ? (uint32_t)(min(WR, u.hi - key) * CB) : 0;
+      const char *kb = khead + from, *vb = vhead + from;
       if constexpr (Q8) {
-        const __amdgpu_buffer_rsrc_t rk = dma::store_rsrc(const_cast<char*>(kb), w.bytes);
-        const __amdgpu_buffer_rsrc_t rv = dma::store_rsrc(const_cast<char*>(vb), w.bytes);
+        const __amdgpu_buffer_rsrc_t rk = dma::store_rsrc(const_cast<char*>(kb), bytes);
+        const __amdgpu_buffer_rsrc_t rv = dma::store_rsrc(const_cast<char*>(vb), bytes);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           kn[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rk, 1024 * i + 16 * lane, 0, 0));
           vn[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rv, 1024 * i + 16 * lane, 0, 0));
         }
       } else {
-        const dma::i32x4 rk = dma::make_rsrc(kb, w.bytes), rv = dma::make_rsrc(vb, w.bytes);
+        const dma::i32x4 rk = dma::make_rsrc(kb, bytes), rv = dma::make_rsrc(vb, bytes);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           const int r = RPL * i + lane / (RB / 16), c = (lane % (RB / 16)) ^ swz<D>(wv * WR + r);
           const uint32_t to = uni(base + stage * M::STAGE + (wv * WR + RPL * i) * RB);
           dma::dma16(rk, r * RB + 16 * c, 0, to);
-          dma::dma16(rv, r * RB + 16 * c, 0, to + M::TILE);
+          dma::dma16(rv, r * RB + 16 * c, 0, to + SUB * M::TILE);
         }
       }
-      if (t + 1 < nt) page_v = page_of(t + 1);
+      page = page_of(t + 1);
     }
     if constexpr (Q8) {
-      // scales: the first wave the keys', the second the values'
+      // scales: the first wave the keys', the second the values'; a key's page, too, is asked for a tile ahead
       if (wv < 2) {
-        sn = 0.f;
         const int key = u.lo + kTile * t + lane;
-        if (key < u.hi) {
-          const int page = p.table[u.seq * p.table_pitch + (key >> p.pshift)];
-          if (page >= 0 && page < p.pages)
-            sn = (wv ? p.vs : p.ks)[((int64_t)page * p.Hk + h) * p.P + (key & (p.P - 1))];
-        }
+        sn = 0.f;
+        if (key < u.hi && (unsigned)key_page < (unsigned)p.pages)
+          sn = (wv ? p.vs : p.ks)[((int64_t)key_page * p.Hk + h) * p.P + (key & (p.P - 1))];
+        key_page = page_of_key(t + 1);
       }
     }
   };
@@ -190,31 +192,44 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
           *reinterpret_cast<bf16x8*>(to + M::TILE + at) = q8_bf16(u32x2v{vn[i][2 * e], vn[i][2 * e + 1]});
         }
       }
-    if (wv < 2) reinterpret_cast<float*>(to + 2 * M::TILE)[wv * kTile + lane] = sn;
+    if (wv < 2) reinterpret_cast<float*>(lds + 2 * M::STAGE + stage * M::SCALES)[wv * kTile + lane] = sn;
   };
+
+  // Tiles [see0, see1) have keys that some of this wave's rows see; all rows see all of tiles [in0, in1).
+  int see0 = nt, see1 = nt, in0 = nt, in1 = nt;
+  {
+    const int r0 = u.row0 + kRows * wv, r1 = min(r0 + kRows, u.row0 + u.nrows) - 1;
+    if (r1 >= r0) {
+      const int last0 = uni(last_key(p, u, r0)), last1 = uni(last_key(p, u, r1));
+      const int first0 = uni(first_key(p, last0)), first1 = uni(first_key(p, last1));
+      see0 = min(nt, max(0, first0 - u.lo) / kTile);
+      see1 = max(see0, min(nt, max(0, last1 - u.lo + kTile) / kTile));
+      in0 = min(nt, max(0, first1 - u.lo + kTile - 1) / kTile);
+      in1 = max(in0, min(nt, max(0, min(last0 + 1, u.hi) - u.lo) / kTile));
+    }
+  }
+
+  // Infinities or NaN among a tile's values: where some rows do not see all of its keys, a product with a weight
+  // of 0 would not be 0.  Such tiles (`odd`: of the masked ones, see0 .. in0 - 1, in1 .. see1 - 1, of which there are
+  // few) are left out and added in the end, key by key.
+  unsigned long long odd = 0;
 
   // Maxima are kept while a new one is less than 2^8 times the old one's weight: outputs and sum are then as
   // exact, and most tiles change nothing.
   const float slack = 8.f / p.scale;
 
-  // One tile.  EDGE: some of its keys are not seen by some of the wave's rows.
-  auto tile = [&](int t, int stage, auto edge_t) {
+  // One tile, number t, the stage's number `sub`.  EDGE: some of its keys are not seen by some of the wave's rows.
+  auto tile = [&](int t, int stage, int sub, auto edge_t) {
     constexpr bool EDGE = decltype(edge_t)::value;
     const int key = u.lo + kTile * t;
-    if constexpr (Q8) land(stage);
-    dma::wait_vm0();
-    __syncthreads();  // this tile is there, and the other stage's readers are done
-    if (t + 1 < nt) ask(t + 1, stage ^ 1);
-    if constexpr (EDGE)
-      if (key > any_last || key + kTile <= any_first) return;  // nothing of it is seen by this wave's rows
-    const int at = stage * M::STAGE;
+    const float* scales = reinterpret_cast<const float*>(lds + 2 * M::STAGE + stage * M::SCALES) + 4 * half;
     f32x16 z[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) z[kb][r] = 0.f;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) z[kb] = mma32(read16(kp[s] + at + 32 * kb * RB), q[s], z[kb]);
+      for (int s = 0; s < KS; ++s) z[kb] = mma32(read16(kp[s] + sub * M::TILE + 32 * kb * RB), q[s], z[kb]);
     }
     if constexpr (!EDGE) {
       // four operands ahead of the products
@@ -226,6 +241,7 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
       }
       __builtin_amdgcn_sched_group_barrier(kMfma, 4, 0);
     }
+    const unsigned from0 = (unsigned)(key + 4 * half - first);
     float top = -__builtin_inff();
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -233,15 +249,12 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
       for (int g = 0; g < 4; ++g) {
         f32x4 ks;
         if constexpr (Q8)
-          ks = *reinterpret_cast<const f32x4*>(lds + at + 2 * M::TILE + 4 * (32 * kb + 8 * g + 4 * half));
+          ks = *reinterpret_cast<const f32x4*>(scales + 32 * kb + 8 * g);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           float x = z[kb][4 * g + r];
           if constexpr (Q8) x *= ks[r];
-          if constexpr (EDGE) {
-            const int k = key + 32 * kb + 8 * g + 4 * half + r;
-            x = k < u.hi && k <= last && k >= first ? x : -__builtin_inff();
-          }
+          if constexpr (EDGE) x = from0 + (unsigned)(32 * kb + 8 * g + r) < seen_n ? x : -__builtin_inff();
           z[kb][4 * g + r] = x;
           top = fmaxf(top, x);
         }
@@ -262,7 +275,7 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
       for (int g = 0; g < 4; ++g) {
         f32x4 vs;
         if constexpr (Q8)
-          vs = *reinterpret_cast<const f32x4*>(lds + at + 2 * M::TILE + 4 * (kTile + 32 * kb + 8 * g + 4 * half));
+          vs = *reinterpret_cast<const f32x4*>(scales + kTile + 32 * kb + 8 * g);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float x = z[kb][4 * g + r];
@@ -276,83 +289,120 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
         }
       }
     auto values = [&](int s, int b) {
-      const u32x2v lo = tr16(vp[0][b] + at + 16 * s * RB), hi = tr16(vp[1][b] + at + 16 * s * RB);
+      const u32x2v lo = tr16(vp[0][b] + sub * M::TILE + 16 * s * RB), hi = tr16(vp[1][b] + sub * M::TILE + 16 * s * RB);
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3));
     };
-    bool odd = false;  // infinities or NaN among values that some rows do not see
-    if constexpr (EDGE) {
-#pragma unroll 1
-      for (int i = 0; i < M::TILE; i += 1024)
-        odd |= not_finite(*reinterpret_cast<const bf16x8*>(lds + at + M::TILE + i + 16 * lane));
-      odd = __ballot(odd) != 0;
+    if (EDGE && (t < in0 || t >= in1)) {
+      unsigned any = 0;
+      const char* v = lds + stage * M::STAGE + (SUB + sub) * M::TILE + 16 * lane;
+#pragma unroll 4
+      for (int i = 0; i < M::TILE; i += 1024) any |= not_finite_bits(*reinterpret_cast<const u32x4v*>(v + i));
+      if (__ballot(any)) {
+        odd |= 1ull << (t < in0 ? t - see0 : t - in1 + (in0 - see0));
+        return;
+      }
     }
-    if (!EDGE || !odd) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int b = 0; b < DB; ++b) o[b] = mma32(values(s, b), pf[s], o[b]);
-      if constexpr (!EDGE && !Q8) {
-        __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 1);
-        __builtin_amdgcn_sched_group_barrier(kValu, 24, 1);
+      for (int b = 0; b < DB; ++b) o[b] = mma32(values(s, b), pf[s], o[b]);
+    if constexpr (!EDGE) {
+      __builtin_amdgcn_sched_group_barrier(kDsRead, Q8 ? 6 : 4, 1);
+      __builtin_amdgcn_sched_group_barrier(kValu, Q8 ? 32 : 24, 1);
 #pragma unroll
-        for (int i = 0; i < 4 * DB; ++i) {
-          __builtin_amdgcn_sched_group_barrier(kMfma, 1, 1);
-          __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 1);
-          __builtin_amdgcn_sched_group_barrier(kValu, 24 / DB, 1);
-        }
+      for (int i = 0; i < 4 * DB; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 1);
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 1);
+        __builtin_amdgcn_sched_group_barrier(kValu, 24 / DB, 1);
       }
-    } else {
-      // a product with a weight of 0 would not be 0: such values are added where they are seen, and taken out
-#pragma unroll
-      for (int b = 0; b < DB; ++b) {
-#pragma unroll 1
-        for (int j = 0; j < kTile; ++j) {
-          const int k = key + j;
-          const bool seen = k < u.hi && k <= last && k >= first;
-          const char* from = lds + at + M::TILE + j * RB + 8 * half;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const u32x2v w = *reinterpret_cast<const u32x2v*>(from + 16 * ((4 * b + g) ^ swz<D>(j)));
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float x = __uint_as_float(r & 1 ? w[r / 2] & 0xffff0000u : w[r / 2] << 16);
-              o[b][4 * g + r] += seen && (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u ? x : 0.f;
-            }
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);  // (rare: few registers before speed)
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int b = 0; b < DB; ++b) {
-          o[b] = mma32(finite_part(values(s, b)), pf[s], o[b]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
     }
   };
 
-  // Tiles [in0, in1) are seen whole by all of the wave's rows; the others, first and last, are masked.
-  int in0 = nt, in1 = nt;
-  if (r1 >= r0) {
-    in0 = min(nt, max(0, all_first - u.lo + kTile - 1) / kTile);
-    in1 = min(nt, max(0, min(all_last + 1, u.hi) - u.lo) / kTile);
-    in0 = (in0 + 1) & ~1;  // (two at a time, in their stages)
-    if (in1 - in0 < 2) in0 = in1 = nt;
-  }
   if (nt) {
     dma::wait_vm0();
     ask(0, 0);
   }
-  int t = 0;
-  for (int end = in0;; end = nt) {
+  // The start of stage n: its tiles are there, and the other stage's readers are done.
+  auto arrive = [&](int n) {
+    if constexpr (Q8) land(n & 1);
+    dma::wait_vm0();
+    __syncthreads();
+    if (n + 1 < ns) ask(n + 1, (n + 1) & 1);
+  };
+  auto leave = [&] {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) kp[s] += hop;
+#pragma unroll
+    for (int b = 0; b < DB; ++b) {
+      vp[0][b] += hop;
+      vp[1][b] += hop;
+    }
+    hop = -hop;
+  };
+  int n = 0;
+  const int n0 = (in0 + SUB - 1) / SUB, n1 = in1 / SUB;  // stages of tiles that all rows see whole
+  for (int end = min(n0, ns);; end = ns) {
 #pragma unroll 1
-    for (; t < end; ++t) tile(t, t & 1, std::true_type{});
-    if (t >= nt) break;
+    for (; n < end; ++n) {
+      arrive(n);
 #pragma unroll 1
-    for (; t + 2 <= in1; t += 2) {
-      tile(t, 0, std::false_type{});
-      tile(t + 1, 1, std::false_type{});
+      for (int sub = 0; sub < SUB; ++sub) {
+        const int t = n * SUB + sub;
+        if (t >= see0 && t < see1) tile(t, n & 1, sub, std::true_type{});
+      }
+      leave();
+    }
+    if (n >= ns) break;
+#pragma unroll 1
+    for (; n < n1; ++n) {
+      arrive(n);
+      static_for<SUB>([&](auto sub) { tile(n * SUB + sub(), n & 1, sub(), std::false_type{}); });
+      leave();
+    }
+  }
+  if (odd) {
+    const float off = m == -__builtin_inff() ? 0.f : -m * p.scale;
+    for (unsigned long long left = odd; left; left &= left - 1) {
+      const int e = __builtin_ctzll(left), t = e < in0 - see0 ? see0 + e : in1 + e - (in0 - see0);
+#pragma unroll 1
+      for (int j = 0; j < kTile; ++j) {
+        const int key = u.lo + kTile * t + j;
+        if (key >= u.hi) break;
+        const Window w = page_rows(p, p.table[u.seq * p.table_pitch + (key >> p.pshift)], h, key, 1, u.hi, CB);
+        const char *kr = static_cast<const char*>(p.k) + w.at, *vr = static_cast<const char*>(p.v) + w.at;
+        if (!w.bytes) continue;  // a page that the cache does not have: values of 0
+        const int64_t place = w.at / CB;
+        float x = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const bf16x8 k8 = Q8 ? q8_bf16(*reinterpret_cast<const u32x2v*>(kr + 16 * s + 8 * half))
+                               : *reinterpret_cast<const bf16x8*>(kr + 32 * s + 16 * half);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x = __builtin_fmaf((float)q[s][i], (float)k8[i], x);
+        }
+        x = add_halves(x);
+        if constexpr (Q8) x *= p.ks[place];
+        float weight = __builtin_amdgcn_exp2f(__builtin_fmaf(x, p.scale, off));
+        if constexpr (Q8) weight *= p.vs[place];
+        weight = (float)(bf16)weight;
+        const bool seen = (unsigned)(key - first) < seen_n;
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int c = 32 * b + 8 * g + 4 * half;
+            float v[4];
+            if constexpr (Q8) {
+              const int w4 = *reinterpret_cast<const int*>(vr + c);
+              const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w4, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w4, true);
+              v[0] = lo[0], v[1] = lo[1], v[2] = hi[0], v[3] = hi[1];
+            } else {
+              loadv<bf16, 4>(reinterpret_cast<const bf16*>(vr) + c, v);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[b][4 * g + r] += seen ? weight * v[r] : 0.f;
+          }
+      }
     }
   }
   m *= p.scale;

@@ -90,16 +90,12 @@ hipError_t join_width(const AttnParams& p, hipStream_t st) {
   return p.D == 64 ? launch_join<T, 64>(p, st) : (p.D == 128 ? launch_join<T, 128>(p, st) : launch_join<T, 256>(p, st));
 }
 
-// Pieces beyond one a unit: as many as fill the chip (`fill` workgroups) where the units do not, and half of
-// that in any case, so that a sequence much longer than the others is cut.  least: tiles of the sequence that
-// has the fewest; if they are as many as the pieces, no sequence is long enough among the others to be cut.
+// Pieces beyond one a unit, so that a piece has about a `fill`-th of all keys of all heads' units.  least: tiles of
+// the sequence that has the fewest; if they are as many as the pieces, none is long enough to be cut.
 int spare_pieces(const AttnPlan& pl, int Hk, int64_t max_keys, int fill, int64_t least) {
   if (!pl.units || 2 * max_keys < 3 * pl.min_piece) return 0;
-  const int64_t have = (int64_t)pl.units * Hk;
-  int64_t want = have < fill ? fill - have : 0;
-  if (want < fill / 2) want = fill / 2;
-  const int64_t spare = (want + Hk - 1) / Hk;
-  return least >= spare ? 0 : (int)spare;
+  const int spare = (fill + Hk - 1) / Hk;
+  return least >= spare ? 0 : spare;
 }
 
 }  // namespace
