@@ -99,8 +99,8 @@ SIGNATURES = {
     "rope_bwd": (I, [P, L, L, P, P, F, P, I, I, I, I, I, I, P]),
     "kv_cache_write": (I, [P, L, L, P, L, L, P, P, P, P, P, I, I, I, I, I, I, I, P]),
     "kv_cache_read": (I, [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]),
-    "paged_attn_workspace_bytes": (SZ, [I, I, I, I, I, I, I, I]),
-    "paged_attn_varlen_workspace_bytes": (SZ, [P, I, I, I, I, I, I, I]),
+    "paged_attn_workspace_bytes": (SZ, [I] * 9),
+    "paged_attn_varlen_workspace_bytes": (SZ, [P] + [I] * 8),
     "paged_attn_fwd": (I, [P, L, L, P, P, P, P, P, L, I, P, F, I, I, P, P] + [I] * 9 + [P, SZ, P]),
     "paged_attn_fwd_varlen": (I, [P, L, L, P, P, P, P, P, L, I, P, P, P, I, F, I, I, P, P] + [I] * 8
                               + [P, SZ, P]),

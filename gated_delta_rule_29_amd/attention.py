@@ -237,7 +237,7 @@ def _attn_args(q, n, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
     if scale is None:
         scale = D ** -0.5 if D else 1.0
     return dev, (q.data_ptr(), pitch, head, *ptrs, block_table.data_ptr(), row if n > 1 else width, width, lp), \
-        scale, Hq, (Hq, Hk, D, pages, P, code, cc), (Hq, Hk, D, P, width, code)
+        scale, Hq, (Hq, Hk, D, pages, P, code, cc), (Hq, Hk, D, P, width, code, cc)
 
 
 def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, k_scale=None, v_scale=None, *, scale=None, causal=True,

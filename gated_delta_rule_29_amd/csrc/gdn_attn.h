@@ -58,7 +58,8 @@ struct AttnPlan {
 // A call's sequences fall into two classes: with at most kFewRows rows (each wave takes its own keys) and
 // with more (each wave takes its own rows).
 constexpr int kFewRows = 32;
-constexpr int many_rows(int D) { return D == 256 ? 128 : 256; }  // of a tile of the second class
+// Rows of a tile of the second class.  256 bf16 columns take twice the registers: one wave a SIMD instead of two.
+constexpr int many_rows(int D, bool q8) { return D == 256 && !q8 ? 128 : 256; }
 enum AttnClass { kAllRows = 0, kFew = 1, kMany = 2 };
 
 struct AttnParams {
@@ -84,7 +85,7 @@ struct AttnParams {
 struct AttnPlans {
   AttnPlan few, many;       // units 0: the class is empty.  fp32: all rows are in `few`
 };
-AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtype, int64_t max_keys);
+AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtype, bool q8, int64_t max_keys);
 size_t attn_ws_bytes(const AttnPlans& pl, int Hk, int D);
 hipError_t launch_attn(AttnParams p, const AttnPlans& pl, int dtype, bool q8, void* ws, hipStream_t st);
 

@@ -127,8 +127,9 @@ int check_attn_rows(const gdn::Seqs& s, const int* cu_host, int G) {
   return GDN_OK;
 }
 
-gdn::AttnPlans plans(const gdn::Seqs& s, const int* cu_host, int Hq, int Hk, int D, int P, int width, int dtype) {
-  return gdn::attn_plans(cu_host, s.n, s.T, Hq / Hk, Hk, D, dtype, (int64_t)width * P);
+gdn::AttnPlans plans(const gdn::Seqs& s, const int* cu_host, int Hq, int Hk, int D, int P, int width, int dtype,
+                     int cache_dtype) {
+  return gdn::attn_plans(cu_host, s.n, s.T, Hq / Hk, Hk, D, dtype, cache_dtype == GDN_DTYPE_E4M3, (int64_t)width * P);
 }
 
 bool odd16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
@@ -151,10 +152,10 @@ int attn(const gdn::Seqs& s, const int* cu_host, const Attn& a, void* ws, size_t
   if (a.window < 0 || (a.window && !a.causal))
     return fail(GDN_ERR_INVALID, "window must be 0 or, in a causal call, positive (got %d)", a.window);
   GDN_TRY(check_attn_rows(s, cu_host, a.Hq / a.Hk));
-  const gdn::AttnPlans pl = plans(s, cu_host, a.Hq, a.Hk, a.D, a.P, a.width, a.dtype);
-  // (512 threads a workgroup at most)
+  const gdn::AttnPlans pl = plans(s, cu_host, a.Hq, a.Hk, a.D, a.P, a.width, a.dtype, a.cache_dtype);
+  // (512 threads a workgroup at most, and two workgroups for 256 columns)
   for (const gdn::AttnPlan& q : {pl.few, pl.many})
-    if (((int64_t)q.units + q.spare) * a.Hk > gdn::kMaxGroups / 2 ||
+    if (((int64_t)q.units + q.spare) * a.Hk > gdn::kMaxGroups / 4 ||
         (int64_t)q.spare * a.Hk * q.part_rows > gdn::kMaxGroups)
       return fail(GDN_ERR_INVALID, "%s of these sizes exceeds the grid limit", what);
   GDN_TRY(check_workspace(ws, ws_bytes, gdn::attn_ws_bytes(pl, a.Hk, a.D)));
@@ -237,19 +238,20 @@ int kv_cache_read(const void* k_cache, const void* v_cache, const float* k_scale
   return e == hipSuccess ? ok() : hip_fail(e, "kv_cache_read launch");
 }
 
-size_t paged_attn_workspace_bytes(int B, int T, int Hq, int Hk, int D, int P, int max_pages, int dtype) {
+size_t paged_attn_workspace_bytes(int B, int T, int Hq, int Hk, int D, int P, int max_pages, int dtype,
+                                  int cache_dtype) {
   gdn::Seqs s;
   if (dense(B, T, &s) || check_attn_sizes(Hq, Hk, D, P, max_pages, dtype) || check_attn_rows(s, nullptr, Hq / Hk)) return 0;
-  return gdn::attn_ws_bytes(plans(s, nullptr, Hq, Hk, D, P, max_pages, dtype), Hk, D);
+  return gdn::attn_ws_bytes(plans(s, nullptr, Hq, Hk, D, P, max_pages, dtype, cache_dtype), Hk, D);
 }
 
 size_t paged_attn_varlen_workspace_bytes(const int* cu_seqlens_host, int N, int Hq, int Hk, int D, int P,
-                                         int max_pages, int dtype) {
+                                         int max_pages, int dtype, int cache_dtype) {
   gdn::Seqs s;
   if (!cu_seqlens_host || N < 1 || packed(cu_seqlens_host, cu_seqlens_host, N, cu_seqlens_host[N], &s) ||
       check_attn_sizes(Hq, Hk, D, P, max_pages, dtype) || check_attn_rows(s, cu_seqlens_host, Hq / Hk))
     return 0;
-  return gdn::attn_ws_bytes(plans(s, cu_seqlens_host, Hq, Hk, D, P, max_pages, dtype), Hk, D);
+  return gdn::attn_ws_bytes(plans(s, cu_seqlens_host, Hq, Hk, D, P, max_pages, dtype, cache_dtype), Hk, D);
 }
 
 int paged_attn_fwd(const void* q, int64_t q_pitch, int64_t q_head, const void* k_cache, const void* v_cache,

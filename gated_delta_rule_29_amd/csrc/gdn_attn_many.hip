@@ -16,7 +16,6 @@ namespace gdn {
 
 namespace {
 
-constexpr int kTile = 64;  // keys of a tile
 // kinds of instructions for the scheduler
 constexpr int kValu = 0x2, kMfma = 0x8, kDsRead = 0x100;
 constexpr int kRows = 32;  // of a wave
@@ -46,33 +45,38 @@ __device__ __forceinline__ int swz(int row) {
 
 template <bool Q8, int D, int NW>
 struct Many {
-  static constexpr int ROWS = kRows * NW;
-  static constexpr int RB = D * 2;
-  static constexpr int TILE = kTile * RB;  // bytes of a tile of keys or values in LDS
+  // Output columns of a workgroup.  256 columns of outputs and queries leave one wave a SIMD, whose 512 registers hold
+  // them with bf16 caches (750 TFLOP/s); 8-bit ones need more, for what is in flight and converted, and are faster (520
+  // against 380) with two workgroups that have half of the outputs each and both form the scores.
+  static constexpr int DV = D == 256 && Q8 ? 128 : D;
+  static constexpr int TK = DV < D ? 32 : 64;  // keys of a tile
+  static constexpr int RK = D * 2, RV = DV * 2;  // bytes of a row of keys and of values in LDS
+  static constexpr int KT = TK * RK, VT = TK * RV;  // and of a tile
   // Tiles that come and go together: with two, the waves meet half as often, and the two of a SIMD drift apart, so that
   // one's products run beside the other's exponentials.
-  static constexpr int SUB = Q8 || D == 256 ? 1 : 2;
-  static constexpr int STAGE = 2 * SUB * TILE;  // keys, then values
-  static constexpr int SCALES = Q8 ? 2 * kTile * 4 : 0;
+  static constexpr int SUB = DV < D || D == 64 || (D == 128 && !Q8) ? 2 : 1;
+  static constexpr int STAGE = SUB * (KT + VT);  // keys, then values
+  static constexpr int SCALES = Q8 ? 2 * SUB * TK * 4 : 0;
   static constexpr int LDS = 2 * (STAGE + SCALES);
 };
 
 template <bool Q8, int D, int NW>
-__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(AttnParams p) {
+__global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   using M = Many<Q8, D, NW>;
-  constexpr int RB = M::RB, CB = Q8 ? D : 2 * D;  // bytes of a row in LDS and in the cache
+  constexpr int RK = M::RK, RV = M::RV, DV = M::DV, CB = Q8 ? D : 2 * D, VB = Q8 ? DV : 2 * DV;  // CB, VB: in the cache
   constexpr int KS = D / 16;                      // contraction steps of the scores
-  constexpr int DB = D / 32;                      // blocks of output columns
-  constexpr int SUB = M::SUB, KEYS = SUB * kTile; // tiles and keys of a stage
-  constexpr int TR = KEYS * CB / 1024;            // 1 KB transfers of a stage's keys
-  constexpr int NI = (TR + NW - 1) / NW;          // of a wave
-  static_assert(TR % NI == 0, "a wave takes NI transfers or none");
-  constexpr int RPL = 1024 / CB;                  // rows of one
+  constexpr int DB = DV / 32;                     // blocks of output columns
+  constexpr int TK = M::TK, SUB = M::SUB, KEYS = SUB * TK;  // keys of a tile; tiles and keys of a stage
+  constexpr int KB = TK / 32, PS = TK / 16;       // blocks of 32 keys, contraction steps of the outputs
+  constexpr int NI = KEYS * CB / 1024 / NW, NV = KEYS * VB / 1024 / NW;  // 1 KB transfers of a wave for a stage
+  constexpr int WR = KEYS / NW;                                           // and its rows
+  static_assert(NI >= 1 && NV >= 1 && WR <= 16, "a wave's rows lie in one page");
   __shared__ __attribute__((aligned(1024))) char lds[M::LDS];
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), col = lane & 31, half = lane >> 5;
-  const int h = blockIdx.x % p.Hk;
+  constexpr int HV = D / DV;
+  const int h = blockIdx.x / HV % p.Hk, c0 = blockIdx.x % HV * DV;  // c0: the first output column
   // descending: a causal sequence's last rows see the most keys
-  const int id = p.plan.units + p.plan.spare - 1 - blockIdx.x / p.Hk;
+  const int id = p.plan.units + p.plan.spare - 1 - blockIdx.x / (HV * p.Hk);
   Unit u;
   if (!find_unit<true>(p, id, lane, &u)) return;
 
@@ -109,90 +113,108 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
 
   const uint32_t base = dma::lds_addr(lds);
   // where a stage's operands are read; the other stage is `hop` away
-  uint32_t kp[KS], vp[2][DB];
+  constexpr int KP = D == 256 ? 1 : KS;  // (256 columns: an XOR with 32 s leads from chunk to chunk)
+  constexpr int VP = DV == 256 ? 1 : DB;
+  uint32_t kp[KP], vp[2][VP];
   int hop = M::STAGE;
   // keys: row col (and 32 more), chunk 2 s + half
 #pragma unroll
-  for (int s = 0; s < KS; ++s) kp[s] = base + col * RB + 16 * ((2 * s + half) ^ swz<D>(col));
+  for (int s = 0; s < KP; ++s) kp[s] = base + col * RK + 16 * ((2 * s + half) ^ swz<D>(col));
   // values, transposing: rows 4 half + (lane & 15) / 4 of each 8, columns 16 ((lane >> 4) & 1) + 4 (lane & 3)
 #pragma unroll
   for (int e = 0; e < 2; ++e)
 #pragma unroll
-    for (int b = 0; b < DB; ++b) {
+    for (int b = 0; b < VP; ++b) {
       const int r = 8 * e + 4 * half + ((lane & 15) >> 2), c = 4 * b + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-      vp[e][b] = base + SUB * M::TILE + r * RB + 16 * (c ^ swz<D>(r)) + 8 * (lane & 1);
+      vp[e][b] = base + SUB * M::KT + r * RV + 16 * (c ^ swz<DV>(r)) + 8 * (lane & 1);
     }
 
-  // Transfers.  A wave has WR rows of a tile, which lie in one page; a page's number is asked for a tile ahead, as
-  // a scalar.
+  // Transfers.  A wave's rows lie in one page, whose number is asked for a stage ahead, as a scalar.
   typedef __attribute__((address_space(4))) const int const_int;
-  constexpr int WR = NI * RPL;
-  const int nt = (u.hi - u.lo + kTile - 1) / kTile, ns = (nt + SUB - 1) / SUB;  // tiles and stages
-  const bool carries = wv * NI < TR;
+  const int nt = (u.hi - u.lo + TK - 1) / TK, ns = (nt + SUB - 1) / SUB;  // tiles and stages
   const_int* table = (const_int*)(uintptr_t)(p.table + u.seq * p.table_pitch);
   const int64_t page_bytes = (int64_t)p.Hk * p.P * CB;
   const char *khead = static_cast<const char*>(p.k) + (int64_t)h * p.P * CB,
-             *vhead = static_cast<const char*>(p.v) + (int64_t)h * p.P * CB;
+             *vhead = static_cast<const char*>(p.v) + (int64_t)h * p.P * CB + c0 * (CB / D);
   auto page_of = [&](int t) { return table[min(u.lo + KEYS * t + wv * WR, u.hi - 1) >> p.pshift]; };
   int page = nt ? page_of(0) : 0;
-  u32x4v kn[Q8 ? NI : 1], vn[Q8 ? NI : 1];
+  u32x4v kn[Q8 ? NI : 1], vn[Q8 ? NV : 1];
   float sn = 0.f;
-  auto page_of_key = [&](int t) { return p.table[u.seq * p.table_pitch + (min(u.lo + kTile * t + lane, u.hi - 1) >> p.pshift)]; };
-  int key_page = Q8 && nt && wv < 2 ? page_of_key(0) : 0;
+  constexpr int SG = KEYS / 64;  // waves that fetch a stage's key scales
+  auto page_of_key = [&](int t) {
+    return p.table[u.seq * p.table_pitch + (min(u.lo + KEYS * t + 64 * (wv % SG) + lane, u.hi - 1) >> p.pshift)];
+  };
+  int key_page = Q8 && nt && wv < 2 * SG ? page_of_key(0) : 0;
 
+  // Lane's part of transfer i of rows of `row` bytes in the cache (of which a transfer takes `part`).
+  auto place = [&](int i, auto part_c, auto row_c) {
+    constexpr int PART = decltype(part_c)::value, LPR = PART / 16;  // lanes of a row
+    return (uint32_t)((1024 / PART * i + lane / LPR) * decltype(row_c)::value + 16 * (lane % LPR));
+  };
+  // The same with the chunk that belongs at lane's place in LDS.
+  auto place_swz = [&](int i, auto d_c, auto row_c) {
+    constexpr int DD = decltype(d_c)::value, LPR = DD / 8;
+    const int r = 512 / DD * i + lane / LPR;
+    return (uint32_t)(r * decltype(row_c)::value + 16 * ((lane % LPR) ^ swz<DD>(wv * WR + r)));
+  };
+  typedef std::integral_constant<int, CB> cb_c;
   auto ask = [&](int t, int stage) {
-    if (carries) {
+    {
       const int key = u.lo + KEYS * t + wv * WR;
       const bool there = key < u.hi && (unsigned)page < (unsigned)p.pages;
       const int64_t from = there ? page * page_bytes + (key & (p.P - 1)) * CB : 0;
       const uint32_t bytes = there ? (uint32_t)(min(WR, u.hi - key) * CB) : 0;
       const char *kb = khead + from, *vb = vhead + from;
+      const uint32_t v_bytes = DV == D || !bytes ? bytes : bytes - c0 * (CB / D);  // (vb is c0 columns in)
       if constexpr (Q8) {
         const __amdgpu_buffer_rsrc_t rk = dma::store_rsrc(const_cast<char*>(kb), bytes);
-        const __amdgpu_buffer_rsrc_t rv = dma::store_rsrc(const_cast<char*>(vb), bytes);
+        const __amdgpu_buffer_rsrc_t rv = dma::store_rsrc(const_cast<char*>(vb), v_bytes);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          kn[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rk, 1024 * i + 16 * lane, 0, 0));
-          vn[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rv, 1024 * i + 16 * lane, 0, 0));
-        }
+        for (int i = 0; i < NI; ++i)
+          kn[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rk, place(i, cb_c{}, cb_c{}), 0, 0));
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          vn[i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(
+                                                 rv, place(i, std::integral_constant<int, VB>{}, cb_c{}), 0, 0));
       } else {
-        const dma::i32x4 rk = dma::make_rsrc(kb, bytes), rv = dma::make_rsrc(vb, bytes);
+        const dma::i32x4 rk = dma::make_rsrc(kb, bytes), rv = dma::make_rsrc(vb, v_bytes);
+        const uint32_t to = uni(base + stage * M::STAGE);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int r = RPL * i + lane / (RB / 16), c = (lane % (RB / 16)) ^ swz<D>(wv * WR + r);
-          const uint32_t to = uni(base + stage * M::STAGE + (wv * WR + RPL * i) * RB);
-          dma::dma16(rk, r * RB + 16 * c, 0, to);
-          dma::dma16(rv, r * RB + 16 * c, 0, to + SUB * M::TILE);
-        }
+        for (int i = 0; i < NI; ++i)
+          dma::dma16(rk, place_swz(i, std::integral_constant<int, D>{}, cb_c{}), 0, to + wv * WR * RK + 1024 * i);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          dma::dma16(rv, place_swz(i, std::integral_constant<int, DV>{}, cb_c{}), 0,
+                     to + SUB * M::KT + wv * WR * RV + 1024 * i);
       }
       page = page_of(t + 1);
     }
     if constexpr (Q8) {
-      // scales: the first wave the keys', the second the values'; a key's page, too, is asked for a tile ahead
-      if (wv < 2) {
-        const int key = u.lo + kTile * t + lane;
+      // scales: the first wave (or two) the keys', the next the values'; a key's page, too, is asked for a stage ahead
+      if (wv < 2 * SG) {
+        const int key = u.lo + KEYS * t + 64 * (wv % SG) + lane;
         sn = 0.f;
         if (key < u.hi && (unsigned)key_page < (unsigned)p.pages)
-          sn = (wv ? p.vs : p.ks)[((int64_t)key_page * p.Hk + h) * p.P + (key & (p.P - 1))];
+          sn = (wv < SG ? p.ks : p.vs)[((int64_t)key_page * p.Hk + h) * p.P + (key & (p.P - 1))];
         key_page = page_of_key(t + 1);
       }
     }
   };
   // 8-bit tiles: from registers into LDS, as bf16
+  auto land_rows = [&](char* to, u32x4v x, int i, auto d_c) {
+    constexpr int DD = decltype(d_c)::value, LPR = DD / 16;
+    const int r = wv * WR + 1024 / DD * i + lane / LPR, c = 2 * (lane % LPR);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      *reinterpret_cast<bf16x8*>(to + r * 2 * DD + 16 * ((c + e) ^ swz<DD>(r))) = q8_bf16(u32x2v{x[2 * e], x[2 * e + 1]});
+  };
   auto land = [&](int stage) {
     char* to = lds + stage * M::STAGE;
-    if (carries)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = (wv * NI + i) * RPL + lane / (D / 16), c = 2 * (lane % (D / 16)), x = swz<D>(r);
+    for (int i = 0; i < NI; ++i) land_rows(to, kn[i], i, std::integral_constant<int, D>{});
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int at = r * RB + 16 * ((c + e) ^ x);
-          *reinterpret_cast<bf16x8*>(to + at) = q8_bf16(u32x2v{kn[i][2 * e], kn[i][2 * e + 1]});
-          *reinterpret_cast<bf16x8*>(to + M::TILE + at) = q8_bf16(u32x2v{vn[i][2 * e], vn[i][2 * e + 1]});
-        }
-      }
-    if (wv < 2) reinterpret_cast<float*>(lds + 2 * M::STAGE + stage * M::SCALES)[wv * kTile + lane] = sn;
+    for (int i = 0; i < NV; ++i) land_rows(to + SUB * M::KT, vn[i], i, std::integral_constant<int, DV>{});
+    if (wv < 2 * SG) reinterpret_cast<float*>(lds + 2 * M::STAGE + stage * M::SCALES)[wv * 64 + lane] = sn;
   };
 
   // Tiles [see0, see1) have keys that some of this wave's rows see; all rows see all of tiles [in0, in1).
@@ -202,10 +224,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
     if (r1 >= r0) {
       const int last0 = uni(last_key(p, u, r0)), last1 = uni(last_key(p, u, r1));
       const int first0 = uni(first_key(p, last0)), first1 = uni(first_key(p, last1));
-      see0 = min(nt, max(0, first0 - u.lo) / kTile);
-      see1 = max(see0, min(nt, max(0, last1 - u.lo + kTile) / kTile));
-      in0 = min(nt, max(0, first1 - u.lo + kTile - 1) / kTile);
-      in1 = max(in0, min(nt, max(0, min(last0 + 1, u.hi) - u.lo) / kTile));
+      see0 = min(nt, max(0, first0 - u.lo) / TK);
+      see1 = max(see0, min(nt, max(0, last1 - u.lo + TK) / TK));
+      in0 = min(nt, max(0, first1 - u.lo + TK - 1) / TK);
+      in1 = max(in0, min(nt, max(0, min(last0 + 1, u.hi) - u.lo) / TK));
     }
   }
 
@@ -218,24 +240,33 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
   // exact, and most tiles change nothing.
   const float slack = 8.f / p.scale;
 
+  auto key_rows = [&](int s, int off) { return read16((KP == 1 ? kp[0] ^ (32 * s) : kp[s % KP]) + off); };
   // One tile, number t, the stage's number `sub`.  EDGE: some of its keys are not seen by some of the wave's rows.
   auto tile = [&](int t, int stage, int sub, auto edge_t) {
     constexpr bool EDGE = decltype(edge_t)::value;
-    const int key = u.lo + kTile * t;
-    const float* scales = reinterpret_cast<const float*>(lds + 2 * M::STAGE + stage * M::SCALES) + 4 * half;
-    f32x16 z[2];
+    const int key = u.lo + TK * t;
+    const float* scales = reinterpret_cast<const float*>(lds + 2 * M::STAGE + stage * M::SCALES) + sub * TK + 4 * half;
+    f32x16 z[2];  // (of one block of keys: even and odd steps, so that a product need not wait for the last one)
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) z[kb][r] = 0.f;
+      for (int r = 0; r < 16; ++r) z[i][r] = 0.f;
+    if constexpr (KB == 2) {
 #pragma unroll
-      for (int s = 0; s < KS; ++s) z[kb] = mma32(read16(kp[s] + sub * M::TILE + 32 * kb * RB), q[s], z[kb]);
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int s = 0; s < KS; ++s) z[kb] = mma32(key_rows(s, sub * M::KT + 32 * kb * RK), q[s], z[kb]);
+    } else {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) z[s & 1] = mma32(key_rows(s, sub * M::KT), q[s], z[s & 1]);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) z[0][r] += z[1][r];
     }
     if constexpr (!EDGE) {
       // four operands ahead of the products
       __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 0);
 #pragma unroll
-      for (int i = 0; i < 2 * KS - 4; ++i) {
+      for (int i = 0; i < KB * KS - 4; ++i) {
         __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
         __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
       }
@@ -244,7 +275,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
     const unsigned from0 = (unsigned)(key + 4 * half - first);
     float top = -__builtin_inff();
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         f32x4 ks;
@@ -268,14 +299,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
       for (int b = 0; b < DB; ++b) o[b] *= a;
     }
     const float off = m == -__builtin_inff() ? 0.f : -m * p.scale;
-    bf16x8 pf[4];
+    bf16x8 pf[PS];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         f32x4 vs;
         if constexpr (Q8)
-          vs = *reinterpret_cast<const f32x4*>(scales + kTile + 32 * kb + 8 * g);
+          vs = *reinterpret_cast<const f32x4*>(scales + KEYS + 32 * kb + 8 * g);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float x = z[kb][4 * g + r];
@@ -289,28 +320,29 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
         }
       }
     auto values = [&](int s, int b) {
-      const u32x2v lo = tr16(vp[0][b] + sub * M::TILE + 16 * s * RB), hi = tr16(vp[1][b] + sub * M::TILE + 16 * s * RB);
+      const int x = VP == 1 ? 64 * b : 0, off = sub * M::VT + 16 * s * RV;
+      const u32x2v lo = tr16((vp[0][b % VP] ^ x) + off), hi = tr16((vp[1][b % VP] ^ x) + off);
       return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3));
     };
     if (EDGE && (t < in0 || t >= in1)) {
       unsigned any = 0;
-      const char* v = lds + stage * M::STAGE + (SUB + sub) * M::TILE + 16 * lane;
+      const char* v = lds + stage * M::STAGE + SUB * M::KT + sub * M::VT + 16 * lane;
 #pragma unroll 4
-      for (int i = 0; i < M::TILE; i += 1024) any |= not_finite_bits(*reinterpret_cast<const u32x4v*>(v + i));
+      for (int i = 0; i < M::VT; i += 1024) any |= not_finite_bits(*reinterpret_cast<const u32x4v*>(v + i));
       if (__ballot(any)) {
         odd |= 1ull << (t < in0 ? t - see0 : t - in1 + (in0 - see0));
         return;
       }
     }
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < PS; ++s)
 #pragma unroll
       for (int b = 0; b < DB; ++b) o[b] = mma32(values(s, b), pf[s], o[b]);
     if constexpr (!EDGE) {
       __builtin_amdgcn_sched_group_barrier(kDsRead, Q8 ? 6 : 4, 1);
       __builtin_amdgcn_sched_group_barrier(kValu, Q8 ? 32 : 24, 1);
 #pragma unroll
-      for (int i = 0; i < 4 * DB; ++i) {
+      for (int i = 0; i < PS * DB; ++i) {
         __builtin_amdgcn_sched_group_barrier(kMfma, 1, 1);
         __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 1);
         __builtin_amdgcn_sched_group_barrier(kValu, 24 / DB, 1);
@@ -331,9 +363,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
   };
   auto leave = [&] {
 #pragma unroll
-    for (int s = 0; s < KS; ++s) kp[s] += hop;
+    for (int s = 0; s < KP; ++s) kp[s] += hop;
 #pragma unroll
-    for (int b = 0; b < DB; ++b) {
+    for (int b = 0; b < VP; ++b) {
       vp[0][b] += hop;
       vp[1][b] += hop;
     }
@@ -365,8 +397,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
     for (unsigned long long left = odd; left; left &= left - 1) {
       const int e = __builtin_ctzll(left), t = e < in0 - see0 ? see0 + e : in1 + e - (in0 - see0);
 #pragma unroll 1
-      for (int j = 0; j < kTile; ++j) {
-        const int key = u.lo + kTile * t + j;
+      for (int j = 0; j < TK; ++j) {
+        const int key = u.lo + TK * t + j;
         if (key >= u.hi) break;
         const Window w = page_rows(p, p.table[u.seq * p.table_pitch + (key >> p.pshift)], h, key, 1, u.hi, CB);
         const char *kr = static_cast<const char*>(p.k) + w.at, *vr = static_cast<const char*>(p.v) + w.at;
@@ -390,7 +422,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
         for (int b = 0; b < DB; ++b)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int c = 32 * b + 8 * g + 4 * half;
+            const int c = c0 + 32 * b + 8 * g + 4 * half;
             float v[4];
             if constexpr (Q8) {
               const int w4 = *reinterpret_cast<const int*>(vr + c);
@@ -413,7 +445,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
   if (u.pieces == 1) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t to = out_row(p, u, h, row);
-    bf16* out = static_cast<bf16*>(p.o) + to * D + 4 * half;
+    bf16* out = static_cast<bf16*>(p.o) + to * D + c0 + 4 * half;
 #pragma unroll
     for (int b = 0; b < DB; ++b)
 #pragma unroll
@@ -421,10 +453,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
         const float r[4] = {o[b][4 * g] * inv, o[b][4 * g + 1] * inv, o[b][4 * g + 2] * inv, o[b][4 * g + 3] * inv};
         storev<bf16, 4>(out + 32 * b + 8 * g, r);
       }
-    if (p.lse && half == 0) p.lse[to] = row_lse(m, l);
+    if (p.lse && half == 0 && c0 == 0) p.lse[to] = row_lse(m, l);
   } else {
     const int at = row - u.row0;
-    float* out = part_outputs(p, u.slot, h) + (int64_t)at * D + 4 * half;
+    float* out = part_outputs(p, u.slot, h) + (int64_t)at * D + c0 + 4 * half;
 #pragma unroll
     for (int b = 0; b < DB; ++b)
 #pragma unroll
@@ -432,7 +464,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
         const float r[4] = {o[b][4 * g], o[b][4 * g + 1], o[b][4 * g + 2], o[b][4 * g + 3]};
         storev<float, 4>(out + 32 * b + 8 * g, r);
       }
-    if (half == 0) {
+    if (half == 0 && c0 == 0) {
       float* s = part_sums(p, u.slot, h) + 2 * at;
       s[0] = m;
       s[1] = l;
@@ -442,8 +474,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_many_kernel(At
 
 template <bool Q8, int D>
 hipError_t launch(const AttnParams& p, hipStream_t st) {
-  constexpr int NW = many_rows(D) / kRows;
-  const int64_t groups = ((int64_t)p.plan.units + p.plan.spare) * p.Hk;
+  constexpr int NW = many_rows(D, Q8) / kRows;
+  const int64_t groups = ((int64_t)p.plan.units + p.plan.spare) * p.Hk * (D / Many<Q8, D, NW>::DV);
   attn_many_kernel<Q8, D, NW><<<dim3((unsigned)groups), 64 * NW, 0, st>>>(p);
   return hipGetLastError();
 }

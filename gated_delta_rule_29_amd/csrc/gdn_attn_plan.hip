@@ -100,11 +100,11 @@ int spare_pieces(const AttnPlan& pl, int Hk, int64_t max_keys, int fill, int64_t
 
 }  // namespace
 
-AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtype, int64_t max_keys) {
+AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtype, bool q8, int64_t max_keys) {
   AttnPlans a{};
   const bool f32 = dtype == GDN_DTYPE_F32;
   const int64_t few_limit = f32 ? INT64_MAX : kFewRows;
-  const int many = many_rows(D);
+  const int many = many_rows(D, q8);
   // (a dense batch's sequences are alike: the first stands for all)
   const int seqs = cu ? n : 1, times = cu ? 1 : n;
   const auto rows_of = [&](int i) { return (int64_t)(cu ? cu[i + 1] - cu[i] : T) * G; };

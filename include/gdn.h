@@ -896,7 +896,7 @@ GDN_API int kv_cache_read(const void* k_cache, const void* v_cache, const float*
  * Supported: D 64, 128 or 256; Hq a multiple of Hk; scale > 0.
  */
 GDN_API size_t paged_attn_workspace_bytes(int B, int T, int Hq, int Hk, int D, int P, int max_pages,
-                                          int dtype);
+                                          int dtype, int cache_dtype);
 GDN_API int paged_attn_fwd(const void* q, int64_t q_pitch, int64_t q_head_pitch, const void* k_cache,
                            const void* v_cache, const float* k_scale, const float* v_scale,
                            const int* block_table, int64_t table_pitch, int max_pages,
@@ -906,7 +906,8 @@ GDN_API int paged_attn_fwd(const void* q, int64_t q_pitch, int64_t q_head_pitch,
 /* The packed form: q, o [1, T_total, Hq, D], lse [1, T_total, Hq], sequence i's new tokens in rows
  * [cu[i], cu[i+1]); block_table [N, max_pages], seq_lens [N]. */
 GDN_API size_t paged_attn_varlen_workspace_bytes(const int* cu_seqlens_host, int N, int Hq, int Hk,
-                                                 int D, int P, int max_pages, int dtype);
+                                                 int D, int P, int max_pages, int dtype,
+                                                 int cache_dtype);
 GDN_API int paged_attn_fwd_varlen(const void* q, int64_t q_pitch, int64_t q_head_pitch,
                                   const void* k_cache, const void* v_cache, const float* k_scale,
                                   const float* v_scale, const int* block_table, int64_t table_pitch,

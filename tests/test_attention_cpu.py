@@ -123,19 +123,19 @@ def test_attention_codes():
 def test_attention_workspace():
     L, lib = _lib()
     # short tables are never cut; long ones need a workspace
-    assert lib.paged_attn_workspace_bytes(2, 1, 4, 2, 64, 16, 4, 1) == 0
-    n = lib.paged_attn_workspace_bytes(2, 1, 4, 2, 64, 16, 400, 1)
+    assert lib.paged_attn_workspace_bytes(2, 1, 4, 2, 64, 16, 4, 1, 1) == 0
+    n = lib.paged_attn_workspace_bytes(2, 1, 4, 2, 64, 16, 400, 1, 1)
     assert n > 0
     assert _step(lib, width=400, tp=400) == L.ERR_WORKSPACE
     assert _step(lib, width=400, tp=400, ws=FAKE, n=n - 1) == L.ERR_WORKSPACE
     assert _step(lib, width=400, tp=400, ws=ctypes.c_void_p(0x1010), n=n) == L.ERR_INVALID  # misaligned
-    assert lib.paged_attn_workspace_bytes(2, 1, 4, 3, 64, 16, 400, 1) == 0  # what cannot be sized
-    assert lib.paged_attn_workspace_bytes(2, 1, 4, 2, 65, 16, 400, 1) == 0
+    assert lib.paged_attn_workspace_bytes(2, 1, 4, 3, 64, 16, 400, 1, 1) == 0  # what cannot be sized
+    assert lib.paged_attn_workspace_bytes(2, 1, 4, 2, 65, 16, 400, 1, 1) == 0
     keep, p = _cu(0, 1, 2)
-    assert lib.paged_attn_varlen_workspace_bytes(p, 2, 4, 2, 64, 16, 400, 1) == n
-    assert lib.paged_attn_varlen_workspace_bytes(None, 2, 4, 2, 64, 16, 400, 1) == 0
+    assert lib.paged_attn_varlen_workspace_bytes(p, 2, 4, 2, 64, 16, 400, 1, 1) == n
+    assert lib.paged_attn_varlen_workspace_bytes(None, 2, 4, 2, 64, 16, 400, 1, 1) == 0
     keep, p = _cu(0, 2, 1)
-    assert lib.paged_attn_varlen_workspace_bytes(p, 2, 4, 2, 64, 16, 400, 1) == 0
+    assert lib.paged_attn_varlen_workspace_bytes(p, 2, 4, 2, 64, 16, 400, 1, 1) == 0
 
 
 def test_binding_refusals():
