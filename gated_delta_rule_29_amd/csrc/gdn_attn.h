@@ -44,11 +44,24 @@ constexpr int kCacheMaxD = 512;
 hipError_t launch_cache_write(const CacheRowsParams& p, int dtype, bool q8, hipStream_t st);
 hipError_t launch_cache_read(const CacheRowsParams& p, int dtype, bool q8, hipStream_t st);
 
+// n / d for n < 2^31 as a product: with 2^(s-1) < d <= 2^s and mul = ceil(2^(31+s) / d), n mul / 2^(31+s) is above
+// n / d by less than 1 / d.  (A kernel of a few microseconds is bound by the instructions that it fetches: a division
+// is 25 of them.)
+struct Divisor {
+  uint32_t mul, shift, by;
+};
+inline Divisor divisor(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t{1} << s) < d) ++s;
+  return Divisor{(uint32_t)(((uint64_t{1} << (31 + s)) + d - 1) / d), 31 + s, d};
+}
+
 // The rows of a sequence and a kv head: its n new tokens times the G query heads that share the head, row
 // token * G + g.  Tiles of rows are the units of work; a unit's keys may be cut into pieces that run at
 // once and are joined.
 struct AttnPlan {
-  int rows;        // of a tile
+  int rows;        // of a tile: 2^row_bits
+  int row_bits;
   int units;       // tiles of all sequences of the class
   int spare;       // pieces beyond one a unit, at most (0: no unit is cut; cut units have 2 * spare at most)
   int min_piece;   // keys
@@ -72,13 +85,14 @@ struct AttnParams {
   Seqs s;
   void* o;                  // [rows, Hq, D]
   float* lse;               // [rows, Hq] or nullptr
-  int Hq, Hk, G, D, pages, P, pshift, width;
+  int Hq, Hk, G, D, pages, P, pshift, width;  // G: query heads of a kv head
   bool q_vec;               // rows of q are aligned to 16 bytes
   float scale;              // of the scores, times log2 e
   bool causal;
   int window;               // 0: none
   int cls;
   AttnPlan plan;
+  Divisor by_heads, by_group, by_tiles;  // kv heads; G; tiles of a sequence of a dense batch
   float* part;              // workspace: outputs [2 * spare][Hk][part_rows][D], then maxima and sums [..][2]
 };
 

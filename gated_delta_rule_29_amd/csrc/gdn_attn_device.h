@@ -29,81 +29,85 @@ __device__ __forceinline__ int attn_tokens(const AttnParams& p, int i) {
 // Tiles of a sequence in the launch's class, and an upper bound of a tile's keys.
 __device__ __forceinline__ int attn_tiles(const AttnParams& p, int rows) {
   if (p.cls != kAllRows && (rows <= kFewRows) != (p.cls == kFew)) return 0;
-  return (rows + p.plan.rows - 1) / p.plan.rows;
+  return (rows + p.plan.rows - 1) >> p.plan.row_bits;
 }
 __device__ __forceinline__ int attn_span(const AttnParams& p, int len) {
-  if (!p.window) return len;
-  const int64_t w = (int64_t)p.window + (p.plan.rows + p.G - 1) / p.G + 64;
-  return (int)min((int64_t)len, w);
+  return p.window ? (int)min((uint32_t)len, (uint32_t)p.window + p.plan.rows + 64) : len;  // (2^31 + 2^9 at most)
 }
 
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// Keys of a piece, about: so many that the units are cut into at most `spare` pieces more than there are units (a
-// unit of n keys into n / keys, rounded: sum of tiles * (pieces - 1) <= sum of tiles * span / keys).  Every wave of every workgroup finds the same number, by itself.
-__device__ __forceinline__ int attn_piece_keys(const AttnParams& p, int lane) {
-  if (p.plan.spare == 0) return 0x7fffffc0;
-  int64_t sum = 0;
-  for (int i = lane; i < p.s.n; i += 64) {
-    sum += (int64_t)attn_tiles(p, attn_tokens(p, i) * p.G) * attn_span(p, attn_len(p, i));
-  }
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) sum += __shfl_xor(sum, off, 64);
-  int64_t keys = (sum + p.plan.spare - 1) / p.plan.spare;
-  if (keys < p.plan.min_piece) keys = p.plan.min_piece;
-  return uni((int)min((keys + 63) & ~int64_t{63}, int64_t{0x7fffffc0}));
+__device__ __forceinline__ int quotient(int n, const Divisor& d) { return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift); }
+
+// Inclusive prefix sum over the wave's lanes: shifts within rows of 16 lanes, then each row's and half's last lane into
+// the next ones.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_shifted(int x) {
+  return x + __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int wave_prefix(int x) {
+  x = add_shifted<0x111, 0xf>(x);
+  x = add_shifted<0x112, 0xf>(x);
+  x = add_shifted<0x114, 0xf>(x);
+  x = add_shifted<0x118, 0xf>(x);
+  x = add_shifted<0x142, 0xa>(x);
+  return add_shifted<0x143, 0xc>(x);
 }
 
-// Pieces of n keys.
-__device__ __forceinline__ int attn_pieces(int n, int keys) { return max(1, (int)(((int64_t)n + keys / 2) / keys)); }
+// Keys of a piece, about: so many that the units are cut into at most `spare` pieces more than there are units (a
+// unit of n keys into n / keys, rounded: sum of tiles * (pieces - 1) <= sum of tiles * span / keys).  Every wave of every workgroup finds
+// the same number, by itself; this is its reciprocal.
+__device__ __forceinline__ float attn_pieces_a_key(const AttnParams& p, int lane) {
+  // (in fp32, every wave in the same order; 2^-7 more keys than that, which 2^23 sequences can be off)
+  float sum = 0.f;
+  for (int i = lane; i < p.s.n; i += 64)
+    sum += (float)attn_tiles(p, attn_tokens(p, i) * p.G) * (float)attn_span(p, attn_len(p, i));
+  const float keys = fmaxf(wave_sum(sum) * (1.f + 0x1p-7f) * __builtin_amdgcn_rcpf((float)p.plan.spare),
+                           (float)p.plan.min_piece);
+  return __uint_as_float((unsigned)uni((int)__float_as_uint(__builtin_amdgcn_rcpf(keys))));
+}
+
+// Pieces of n keys, each of about 1 / inv.
+__device__ __forceinline__ int attn_pieces(int n, float inv) { return max(1, (int)__builtin_fmaf((float)n, inv, 0.5f)); }
 
 // Finds piece number `id` (PIECES), or the first piece of unit number `id` of those that may be cut; false where
 // there is nothing to do.
 template <bool PIECES>
 __device__ __forceinline__ bool find_unit(const AttnParams& p, int id, int lane, Unit* u) {
-  const int keys = attn_piece_keys(p, lane);
+  const float inv = p.plan.spare ? attn_pieces_a_key(p, lane) : 0.f;
   int before = 0, before_cut = 0;  // what is counted, and cut units' pieces, of the sequences looked at
   int seq = -1, at = 0, cut_at = 0, per_tile = 1;
   if (p.plan.spare == 0 && !p.s.cu) {  // sequences alike
-    const int tiles = (p.s.T * p.G + p.plan.rows - 1) / p.plan.rows;
-    seq = id / tiles;
+    seq = quotient(id, p.by_tiles);
     if (seq >= p.s.n) return false;
-    at = seq * tiles;
+    at = seq * p.by_tiles.by;
   } else {
     for (int base = 0; base < p.s.n && seq < 0; base += 64) {
       const int i = base + lane;
       int tiles = 0, k = 1;
       if (i < p.s.n) {
         tiles = attn_tiles(p, attn_tokens(p, i) * p.G);
-        if (p.plan.spare) k = attn_pieces(attn_span(p, attn_len(p, i)), keys);
+        if (p.plan.spare) k = attn_pieces(attn_span(p, attn_len(p, i)), inv);
       }
       const int cut = k > 1 ? tiles * k : 0, mine = PIECES ? tiles * k : (k > 1 ? tiles : 0);
-      int sum = mine, sum_cut = cut;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int a = __shfl_up(sum, off, 64), b = __shfl_up(sum_cut, off, 64);
-        if (lane >= off) {
-          sum += a;
-          sum_cut += b;
-        }
-      }
+      const int sum = wave_prefix(mine), sum_cut = wave_prefix(cut);
       const unsigned long long m = __ballot(id < before + sum && id >= before + sum - mine);
       if (m) {
         const int l = __builtin_ctzll(m);
         seq = base + l;
-        per_tile = uni(__shfl(k, l, 64));
-        at = before + uni(__shfl(sum - mine, l, 64));
-        cut_at = before_cut + uni(__shfl(sum_cut - cut, l, 64));
+        per_tile = __builtin_amdgcn_readlane(k, l);
+        at = before + __builtin_amdgcn_readlane(sum - mine, l);
+        cut_at = before_cut + __builtin_amdgcn_readlane(sum_cut - cut, l);
       }
-      before += uni(__shfl(sum, 63, 64));
-      before_cut += uni(__shfl(sum_cut, 63, 64));
+      before += __builtin_amdgcn_readlane(sum, 63);
+      before_cut += __builtin_amdgcn_readlane(sum_cut, 63);
     }
     if (seq < 0) return false;
   }
   seq = uni(seq);
   const int off = PIECES ? id - at : (id - at) * per_tile;
   u->seq = seq;
-  u->tile = off / per_tile;
+  u->tile = per_tile == 1 ? off : off / per_tile;
   u->piece = off - u->tile * per_tile;
   u->slot = cut_at + off;
   u->begin = uni(seq_begin(p.s, seq));
@@ -114,13 +118,13 @@ __device__ __forceinline__ bool find_unit(const AttnParams& p, int id, int lane,
   // the keys that any of the rows sees, and this piece's share of them
   int base = 0, end = u->len;
   if (p.causal) {
-    end = max(0, min(end, u->len - u->n + (u->row0 + u->nrows - 1) / p.G + 1));
-    if (p.window) base = min(end, max(0, u->len - u->n + u->row0 / p.G - p.window + 1)) & ~63;
+    end = max(0, min(end, u->len - u->n + quotient(u->row0 + u->nrows - 1, p.by_group) + 1));
+    if (p.window) base = min(end, max(0, u->len - u->n + quotient(u->row0, p.by_group) - p.window + 1)) & ~63;
   }
   // (a causal sequence's first tiles see fewer keys than its last one, and may have fewer pieces)
-  u->pieces = p.plan.spare ? min(per_tile, attn_pieces(end - base, keys)) : 1;
+  u->pieces = p.plan.spare ? uni(min(per_tile, attn_pieces(end - base, inv))) : 1;
   if (PIECES ? u->piece >= u->pieces : u->pieces == 1) return false;
-  const int share = ((end - base + u->pieces - 1) / u->pieces + 63) & ~63;
+  const int share = u->pieces == 1 ? (end - base + 63) & ~63 : ((end - base + u->pieces - 1) / u->pieces + 63) & ~63;
   const int64_t lo = base + (int64_t)u->piece * share;
   u->lo = (int)min(lo, (int64_t)end);
   u->hi = (int)min(lo + share, (int64_t)end);
@@ -129,7 +133,7 @@ __device__ __forceinline__ bool find_unit(const AttnParams& p, int id, int lane,
 
 // The last key that row `row` of the unit's sequence sees, and the first.
 __device__ __forceinline__ int last_key(const AttnParams& p, const Unit& u, int row) {
-  return p.causal ? min(u.len - 1, u.len - u.n + row / p.G) : u.len - 1;
+  return p.causal ? min(u.len - 1, u.len - u.n + quotient(row, p.by_group)) : u.len - 1;
 }
 __device__ __forceinline__ int first_key(const AttnParams& p, int last) {
   return p.window ? max(0, last - p.window + 1) : 0;  // (an empty row's last key is negative)
@@ -187,7 +191,7 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 
 // Index of output row (token of the batch, query head) of the unit's row.
 __device__ __forceinline__ int64_t out_row(const AttnParams& p, const Unit& u, int h, int row) {
-  const int t = row / p.G;
+  const int t = quotient(row, p.by_group);
   return (int64_t)(u.begin + t) * p.Hq + h * p.G + (row - t * p.G);
 }
 // Partial results of a piece: its rows' outputs, and their maxima and sums.

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnParams p) {
   constexpr int RPL = 1024 / CB;                  // rows of one
   __shared__ __attribute__((aligned(1024))) char lds[F::LDS];
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), li = lane & 15, lq = lane >> 4;
-  const int id = blockIdx.x / p.Hk, h = blockIdx.x % p.Hk;
+  const int id = quotient(blockIdx.x, p.by_heads), h = blockIdx.x - id * p.Hk;
   Unit u;
   if (!find_unit<true>(p, id, lane, &u)) return;
 
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnParams p) {
     const int row = u.row0 + 16 * mt + li;
     last[mt] = last_key(p, u, row);
     first[mt] = first_key(p, last[mt]);
-    const int t = row / p.G;
+    const int t = quotient(row, p.by_group);
     const bf16* from = static_cast<const bf16*>(p.q.p) + (int64_t)(u.begin + t) * p.q.pitch +
                        (h * p.G + row - t * p.G) * p.q.head;
 #pragma unroll

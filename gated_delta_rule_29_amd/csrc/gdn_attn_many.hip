@@ -74,9 +74,9 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   __shared__ __attribute__((aligned(1024))) char lds[M::LDS];
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), col = lane & 31, half = lane >> 5;
   constexpr int HV = D / DV;
-  const int h = blockIdx.x / HV % p.Hk, c0 = blockIdx.x % HV * DV;  // c0: the first output column
-  // descending: a causal sequence's last rows see the most keys
-  const int id = p.plan.units + p.plan.spare - 1 - blockIdx.x / (HV * p.Hk);
+  const int uh = blockIdx.x / HV, up = quotient(uh, p.by_heads);
+  const int h = uh - up * p.Hk, c0 = blockIdx.x % HV * DV;  // c0: the first output column
+  const int id = p.plan.units + p.plan.spare - 1 - up;      // descending: a causal sequence's last rows see the most keys
   Unit u;
   if (!find_unit<true>(p, id, lane, &u)) return;
 
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   const unsigned seen_n = (unsigned)max(0, min(last, u.hi - 1) - first + 1);  // keys of this piece from `first` on
   bf16x8 q[KS];
   {
-    const int t = row / p.G;
+    const int t = quotient(row, p.by_group);
     const bf16* from = static_cast<const bf16*>(p.q.p) + (int64_t)(u.begin + t) * p.q.pitch +
                        (h * p.G + row - t * p.G) * p.q.head + 8 * half;
 #pragma unroll

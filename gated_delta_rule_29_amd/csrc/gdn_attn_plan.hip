@@ -12,17 +12,17 @@ namespace {
 // four times groups that take every so-many-th piece, joined in LDS in a fixed order.  A workgroup takes `rows`
 // rows of a unit: most workgroups of a call that cuts little find nothing to do, so they are few.
 template <typename T, int D, int RPW>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p, int per_unit, int rows) {
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p, Divisor per_unit, int rows) {
   constexpr int TEAM = 256 / RPW, LP = D / 4, GR = TEAM / LP;
   __shared__ float acc[RPW][GR][D + 2];
   const int lane = threadIdx.x & 63;
   const int sub = threadIdx.x / TEAM, tid = threadIdx.x % TEAM, g = tid / LP, c = (tid % LP) * 4;
-  const int h = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk, id = rest / per_unit;
+  const int rest = quotient(blockIdx.x, p.by_heads), h = blockIdx.x - rest * p.Hk, id = quotient(rest, per_unit);
   Unit u;
   if (!find_unit<false>(p, id, lane, &u)) return;
   const int pieces = min(u.pieces, 2 * p.plan.spare - u.slot);  // (fewer only with other offsets than the host's)
   const int64_t step = (int64_t)p.Hk * p.plan.part_rows;  // rows from piece to piece
-  const int first = (rest - id * per_unit) * rows, end = min(first + rows, u.nrows);
+  const int first = (rest - id * (int)per_unit.by) * rows, end = min(first + rows, u.nrows);
   for (int at0 = first; at0 < end; at0 += RPW) {
     const int at = at0 + sub;
     const float* part = part_outputs(p, u.slot, h) + (int64_t)at * D + c;
@@ -77,12 +77,13 @@ template <typename T, int D>
 hipError_t launch_join(const AttnParams& p, hipStream_t st) {
   // one row a workgroup where rows are few and pieces many
   const bool few = p.plan.part_rows <= kFewRows;
-  const int rows = few ? 1 : 32, per_unit = (p.plan.part_rows + rows - 1) / rows;
+  constexpr int RPW = 1024 / D;  // rows at a time, a group of threads each
+  const int rows = few ? 1 : 2 * RPW, per_unit = (p.plan.part_rows + rows - 1) / rows;
   // (there are at most `spare` cut units)
   const int64_t groups = (int64_t)(p.plan.units < p.plan.spare ? p.plan.units : p.plan.spare) * p.Hk * per_unit;
   if (groups > kMaxGroups) return hipErrorInvalidConfiguration;
-  if (few) attn_join_kernel<T, D, 1><<<dim3((unsigned)groups), 256, 0, st>>>(p, per_unit, rows);
-  else attn_join_kernel<T, D, 4><<<dim3((unsigned)groups), 256, 0, st>>>(p, per_unit, rows);
+  if (few) attn_join_kernel<T, D, 1><<<dim3((unsigned)groups), 256, 0, st>>>(p, divisor(per_unit), rows);
+  else attn_join_kernel<T, D, RPW><<<dim3((unsigned)groups), 256, 0, st>>>(p, divisor(per_unit), rows);
   return hipGetLastError();
 }
 template <typename T>
@@ -121,7 +122,8 @@ AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtyp
     }
   }
   // 32-row tiles of 256 columns would not fit into registers
-  a.few.rows = most_few <= 16 || D == 256 ? 16 : 32;
+  a.few.row_bits = most_few <= 16 || D == 256 ? 4 : 5;
+  a.few.rows = 1 << a.few.row_bits;
   int64_t units_few = 0, least_few = INT64_MAX;
   for (int i = 0; most_few && i < seqs; ++i) {
     const int64_t rows = rows_of(i);
@@ -136,10 +138,11 @@ AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtyp
   a.few.min_piece = 512;
   a.few.spare = spare_pieces(a.few, Hk, max_keys, 1024, least_few);
   a.many.rows = many;
+  a.many.row_bits = __builtin_ctz((unsigned)many);
   a.many.units = (int)(units_many < most ? units_many : most);
   a.many.part_rows = (int)(most_many < many ? most_many : many);
   a.many.min_piece = 1024;
-  a.many.spare = spare_pieces(a.many, Hk, max_keys, 512, least_many);
+  a.many.spare = spare_pieces(a.many, Hk, max_keys, 256, least_many);
   return a;
 }
 
@@ -156,9 +159,13 @@ hipError_t launch_attn_join(const AttnParams& p, int dtype, hipStream_t st) {
 
 hipError_t launch_attn(AttnParams p, const AttnPlans& pl, int dtype, bool q8, void* ws, hipStream_t st) {
   char* at = static_cast<char*>(ws);
+  p.by_heads = divisor((uint32_t)p.Hk);
+  p.by_group = divisor((uint32_t)p.G);
   for (int many = 1; many >= 0; --many) {  // the class with more work goes first
     p.plan = many ? pl.many : pl.few;
     if (!p.plan.units) continue;
+    // (T is 0 in a packed batch, whose tiles are looked for)
+    p.by_tiles = divisor(p.s.cu ? 1u : (uint32_t)(((int64_t)p.s.T * p.G + p.plan.rows - 1) >> p.plan.row_bits));
     p.cls = dtype == GDN_DTYPE_F32 || !(many ? pl.few : pl.many).units ? kAllRows : (many ? kMany : kFew);
     p.part = reinterpret_cast<float*>(at);
     at += part_bytes(p.plan, p.Hk, p.D);
