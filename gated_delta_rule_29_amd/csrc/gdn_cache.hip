@@ -4,7 +4,11 @@
 //   8 bits: scale = max(max |x|, 1e-12) / 448 over a head's D columns, q = e4m3(x / scale)
 //
 // A row (one token and head) is held by 8 to 64 lanes, 8 columns each, so that the scale's maximum is a
-// lane exchange and every input is read once.  Bound by memory.
+// lane exchange and every input is read once.  Reading is bound by memory (16384 tokens of 8 heads of 128 columns out
+// of pages of 16: 17.5 us, 5.8 TB/s of what it reads and writes, part of it out of the last caches).  Writing 8 bits
+// is bound by its instructions, about 1050 a wave and 4 rows: addresses in 64 bits, the maximum, conversions, and the
+// look through earlier slots (8192 tokens of 8 heads of 128 columns: 21 us, 2.5 TB/s).  16 columns a lane, and
+// neighbouring tokens on one die, were no faster.  Single tokens (64 of them: 4.4 us) are one chain of loads.
 #include "../../include/gdn.h"
 #include "gdn_attn.h"
 #include "gdn_layer_device.h"
@@ -16,33 +20,49 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 8 columns c .. c + 7 of a row of D as fp32, 0 beyond it.
+// Columns c .. c + 7 of a row of D, 0 beyond it: as they are in memory while they are on their way (a
+// conversion would wait for them), and as fp32.  VEC: in 16-byte accesses.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_row8(const T* p, int c, int D, float (&x)[8]) {
-  if constexpr (VEC) {
-    if (c < D) {
-      load8f(p + c, x);
-    } else {
+struct Row8 {
+  u32x4v v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, int c, int D) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = c + i < D ? to_f(p[c + i]) : 0.f;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      if (c + i * 16 / (int)sizeof(T) < D) v[i] = reinterpret_cast<const u32x4v*>(p + c)[i];
   }
-}
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(v[i / 4][i % 4]);
+      else x[i] = __uint_as_float(i & 1 ? v[i / 8][i % 8 / 2] & 0xffff0000u : v[i / 8][i % 8 / 2] << 16);
+    }
+  }
+};
+template <typename T>
+struct Row8<T, false> {
+  T v[8];
+  __device__ __forceinline__ void load(const T* p, int c, int D) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < D) v[i] = p[c + i];
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f(v[i]);
+  }
+};
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_row8(T* p, int c, int D, const float (&x)[8]) {
   if constexpr (VEC) {
-    if (c < D) {
-      if constexpr (sizeof(T) == 4) {
-        const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
-        storev<T, 4>(p + c, a);
-        storev<T, 4>(p + c + 4, b);
-      } else {
-        storev<T, 8>(p + c, x);
+    constexpr int W = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < 8; i += W)
+      if (c + i < D) {
+        float w[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j] = x[i + j];
+        storev<T, W>(p + c + i, w);
       }
-    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -74,27 +94,49 @@ __device__ __forceinline__ unsigned lanes_max(unsigned x) {
 // LDS atomics, whose order does not change it.
 constexpr int kMapWords = 1024;
 constexpr int kMaxTokens = 64;
-__device__ __forceinline__ void find_live(const int* slots, int t0, int n, int limit, int* own, int* dead,
+constexpr int kLook = 8;  // earlier slots that a thread asks for together
+struct Slots {
+  int mine, s[kLook];
+};
+__device__ __forceinline__ Slots ask_slots(const int* slots, int t0, int n) {
+  Slots r;
+  r.mine = (int)threadIdx.x < n ? slots[t0 + threadIdx.x] : -1;
+#pragma unroll
+  for (int e = 0; e < kLook; ++e) {
+    const int i = (int)threadIdx.x + e * kThreads;
+    r.s[e] = i < t0 + n ? slots[i] : -1;
+  }
+  return r;
+}
+__device__ __forceinline__ void find_live(const int* slots, Slots r, int t0, int n, int limit, int* own, int* dead,
                                           unsigned* map) {
   for (int i = threadIdx.x; i < kMapWords; i += kThreads) map[i] = 0;
+  int(&s)[kLook] = r.s;
+  const int mine = r.mine;
   __syncthreads();
   if ((int)threadIdx.x < n) {
-    const int s = slots[t0 + threadIdx.x];
-    own[threadIdx.x] = s;
-    dead[threadIdx.x] = s < 0 || s >= limit;
-    atomicOr(&map[(s >> 5) & (kMapWords - 1)], 1u << (s & 31));
+    own[threadIdx.x] = mine;
+    dead[threadIdx.x] = mine < 0 || mine >= limit;
+    atomicOr(&map[(mine >> 5) & (kMapWords - 1)], 1u << (mine & 31));
   }
   __syncthreads();
-  const int end = t0 + n;
-  for (int b = threadIdx.x * 4; b < end; b += kThreads * 4) {
-    int s[4];
+  for (int b = threadIdx.x;; b += kLook * kThreads) {
+    unsigned hits = 0;  // (a slot of -1, behind the end, may hit too)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = b + e < end ? slots[b + e] : -1;
+    for (int e = 0; e < kLook; ++e) hits |= (map[(s[e] >> 5) & (kMapWords - 1)] >> (s[e] & 31) & 1) << e;
+    for (; hits; hits &= hits - 1) {
+      const int i = b + __builtin_ctz(hits) * kThreads;
+      if (i >= t0 + n) break;
+      const int slot = slots[i];
+      for (int j = max(i + 1 - t0, 0); j < n; ++j)
+        if (own[j] == slot) dead[j] = 1;
+    }
+    if (b + kLook * kThreads >= t0 + n) break;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (map[(s[e] >> 5) & (kMapWords - 1)] >> (s[e] & 31) & 1)
-        for (int j = max(b + e + 1 - t0, 0); j < n; ++j)
-          if (own[j] == s[e]) dead[j] = 1;
+    for (int e = 0; e < kLook; ++e) {
+      const int i = b + (kLook + e) * kThreads;
+      s[e] = i < t0 + n ? slots[i] : -1;
+    }
   }
   __syncthreads();
 }
@@ -104,55 +146,68 @@ __device__ __forceinline__ void find_live(const int* slots, int t0, int n, int l
 constexpr int kBatch = 4;
 struct Row {
   int t, h;
-  bool val, live;
-  int64_t at;  // in the cache
+  bool val, there;
 };
-__device__ __forceinline__ Row row_of(const CacheRowsParams& p, int r, int rows, int nh, int h0, const int* slot,
-                                      const int* dead) {
+struct RowGrid {
+  int tokens, heads;     // of a workgroup
+  Divisor groups, pair;  // workgroups for the heads of a token; 2 * heads
+  int pshift;            // a page has 2^pshift places
+};
+__device__ __forceinline__ int quotient(int n, const Divisor& d) { return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift); }
+__device__ __forceinline__ Row row_of(const CacheRowsParams& p, const RowGrid& g, int r, int rows, int h0) {
   Row w;
-  w.t = r / (2 * nh);
-  const int hv = r - w.t * 2 * nh;
-  w.val = hv >= nh;
-  w.h = h0 + (w.val ? hv - nh : hv);
-  w.live = r < rows;
-  const int s = w.live ? slot[w.t] : 0;
-  w.live = w.live && !(dead ? dead[w.t] : s < 0 || s >= p.c.pages * p.c.P);
-  const int page = w.live ? s / p.c.P : 0, place = w.live ? s - page * p.c.P : 0;
-  w.at = ((int64_t)page * p.c.H + w.h) * p.c.P + place;
+  w.t = quotient(r, g.pair);
+  const int hv = r - w.t * (int)g.pair.by;
+  w.val = hv >= g.heads;
+  w.h = h0 + (w.val ? hv - g.heads : hv);
+  w.there = r < rows && w.h < p.c.H;
   return w;
+}
+__device__ __forceinline__ int64_t cache_row(const Cache& c, int pshift, int slot, int h) {
+  const int page = slot >> pshift;
+  return ((int64_t)page * c.H + h) * c.P + (slot - (page << pshift));
 }
 
 template <typename T, bool Q8, bool VEC, int LPR>
-__global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheRowsParams p, int tokens, int heads, int groups) {
+__global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheRowsParams p, RowGrid g) {
   __shared__ int own[kMaxTokens], dead[kMaxTokens];
   __shared__ unsigned map[kMapWords];
-  const int t0 = (blockIdx.x / groups) * tokens, h0 = (blockIdx.x % groups) * heads;
-  const int nt = min(tokens, p.T - t0), nh = min(heads, p.c.H - h0);
-  find_live(p.slots, t0, nt, p.c.pages * p.c.P, own, dead, map);
+  const int tile = quotient(blockIdx.x, g.groups), t0 = tile * g.tokens;
+  const int h0 = (blockIdx.x - tile * (int)g.groups.by) * g.heads, nt = min(g.tokens, p.T - t0);
   const int c = (threadIdx.x % LPR) * 8;
-  const int rows = nt * nh * 2;
+  const int rows = nt * g.heads * 2;
   constexpr int STEP = kThreads / LPR;
-  for (int r0 = threadIdx.x / LPR; r0 < rows; r0 += kBatch * STEP) {
-    float x[kBatch][8];
-    Row w[kBatch];
+  Row8<T, VEC> in[kBatch];
+  Row w[kBatch];
+  auto ask = [&](int r0) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      w[b] = row_of(p, r0 + b * STEP, rows, nh, h0, own, dead);
-      const Heads& in = w[b].val ? p.v : p.k;
-      if (w[b].live)
-        load_row8<T, VEC>(static_cast<const T*>(in.p) + (t0 + w[b].t) * in.pitch + w[b].h * in.head, c, p.c.D, x[b]);
+      w[b] = row_of(p, g, r0 + b * STEP, rows, h0);
+      const Heads& from = w[b].val ? p.v : p.k;
+      in[b] = {};
+      if (w[b].there)
+        in[b].load(static_cast<const T*>(from.p) + (t0 + w[b].t) * from.pitch + w[b].h * from.head, c, p.c.D);
     }
+  };
+  int r0 = threadIdx.x / LPR;
+  const Slots slots = ask_slots(p.slots, t0, nt);
+  ask(r0);  // (under way while the slots are looked through)
+  find_live(p.slots, slots, t0, nt, p.c.pages * p.c.P, own, dead, map);
+  while (r0 < rows) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      if (!w[b].live) continue;
+      if (!w[b].there || dead[w[b].t]) continue;
+      const int64_t at = cache_row(p.c, g.pshift, own[w[b].t], w[b].h);
       void* to = w[b].val ? p.c.v : p.c.k;
+      float x[8];
+      in[b].values(x);
       if constexpr (Q8) {
         unsigned m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[b][i]) & 0x7fffffffu);  // a NaN is above all
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);  // a NaN is above all
         const float scale = q8_scale(lanes_max<LPR>(m));
-        uint8_t* q = static_cast<uint8_t*>(to) + w[b].at * p.c.D;
-        const u32x2v v = q8_pack(x[b], scale);
+        uint8_t* q = static_cast<uint8_t*>(to) + at * p.c.D;
+        const u32x2v v = q8_pack(x, scale);
         if constexpr (VEC) {
           if (c < p.c.D) *reinterpret_cast<u32x2v*>(q + c) = v;
         } else {
@@ -160,37 +215,41 @@ __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheRowsParams p
           for (int i = 0; i < 8; ++i)
             if (c + i < p.c.D) q[c + i] = (uint8_t)(v[i / 4] >> (8 * (i % 4)));
         }
-        if (c == 0) (w[b].val ? p.c.vs : p.c.ks)[w[b].at] = scale;
+        if (c == 0) (w[b].val ? p.c.vs : p.c.ks)[at] = scale;
       } else {
-        store_row8<T, VEC>(static_cast<T*>(to) + w[b].at * p.c.D, c, p.c.D, x[b]);
+        store_row8<T, VEC>(static_cast<T*>(to) + at * p.c.D, c, p.c.D, x);
       }
     }
+    r0 += kBatch * STEP;
+    if (r0 < rows) ask(r0);
   }
 }
 
 template <typename T, bool Q8, bool VEC, int LPR>
-__global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheRowsParams p, int tokens, int heads, int groups) {
-  const int t0 = (blockIdx.x / groups) * tokens, h0 = (blockIdx.x % groups) * heads;
-  const int nt = min(tokens, p.T - t0), nh = min(heads, p.c.H - h0);
+__global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheRowsParams p, RowGrid g) {
+  const int tile = quotient(blockIdx.x, g.groups), t0 = tile * g.tokens;
+  const int h0 = (blockIdx.x - tile * (int)g.groups.by) * g.heads, nt = min(g.tokens, p.T - t0);
   const int c = (threadIdx.x % LPR) * 8;
-  const int rows = nt * nh * 2;
+  const int rows = nt * g.heads * 2;
   constexpr int STEP = kThreads / LPR;
   for (int r0 = threadIdx.x / LPR; r0 < rows; r0 += kBatch * STEP) {
-    float x[kBatch][8], scale[kBatch];
+    float scale[kBatch];
     u32x2v q[kBatch];
+    Row8<T, VEC> in[kBatch];
     Row w[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      w[b] = row_of(p, r0 + b * STEP, rows, nh, h0, p.slots + t0, nullptr);
+      w[b] = row_of(p, g, r0 + b * STEP, rows, h0);
       const void* from = w[b].val ? p.c.v : p.c.k;
       q[b] = u32x2v{0u, 0u};
       scale[b] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[b][i] = 0.f;
-      if (!w[b].live) continue;
+      in[b] = {};
+      const int slot = w[b].there ? p.slots[t0 + w[b].t] : -1;
+      if (slot < 0 || slot >= p.c.pages * p.c.P) continue;
+      const int64_t at = cache_row(p.c, g.pshift, slot, w[b].h);
       if constexpr (Q8) {
-        const uint8_t* row = static_cast<const uint8_t*>(from) + w[b].at * p.c.D;
-        scale[b] = (w[b].val ? p.c.vs : p.c.ks)[w[b].at];
+        const uint8_t* row = static_cast<const uint8_t*>(from) + at * p.c.D;
+        scale[b] = (w[b].val ? p.c.vs : p.c.ks)[at];
         if constexpr (VEC) {
           if (c < p.c.D) q[b] = *reinterpret_cast<const u32x2v*>(row + c);
         } else {
@@ -199,34 +258,34 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheRowsParams p,
             if (c + i < p.c.D) q[b][i / 4] |= (unsigned)row[c + i] << (8 * (i % 4));
         }
       } else {
-        load_row8<T, VEC>(static_cast<const T*>(from) + w[b].at * p.c.D, c, p.c.D, x[b]);
+        in[b].load(static_cast<const T*>(from) + at * p.c.D, c, p.c.D);
       }
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      if (r0 + b * STEP >= rows) continue;
+      if (!w[b].there) continue;
+      float x[8];
       if constexpr (Q8) {
-        q8_unpack(q[b], x[b]);
+        q8_unpack(q[b], x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[b][i] *= scale[b];
+        for (int i = 0; i < 8; ++i) x[i] *= scale[b];
+      } else {
+        in[b].values(x);
       }
       T* to = static_cast<T*>(w[b].val ? p.vo : p.ko) + ((int64_t)(t0 + w[b].t) * p.c.H + w[b].h) * p.c.D;
-      store_row8<T, VEC>(to, c, p.c.D, x[b]);
+      store_row8<T, VEC>(to, c, p.c.D, x);
     }
   }
 }
 
 template <typename T, bool Q8, bool VEC, bool WRITE, int LPR>
 hipError_t launch(const CacheRowsParams& p, hipStream_t st) {
-  // Tokens of a workgroup: enough rows for four rounds of its lanes where that still fills the chip; for
-  // writing, more in very long calls, where each workgroup looks through all earlier slots.
+  // Tokens of a workgroup: as many rows as its lanes ask for together, where that still fills the chip.  Writing looks
+  // through all earlier slots in every workgroup: more tokens in very long calls.
   const int per = kThreads / LPR;  // rows at a time
   int tokens = 1;
-  while (tokens < 16 && tokens * 2 * p.c.H < 4 * per && p.T / (2 * tokens) >= 512) tokens *= 2;
-  if (WRITE) {
-    if (p.T > 2048 && tokens < 16) tokens = 16;
-    if (p.T > 16384) tokens = kMaxTokens;
-  }
+  while (tokens < 16 && tokens * 4 * p.c.H <= kBatch * per && p.T / (2 * tokens) >= 512) tokens *= 2;
+  if (WRITE && p.T > 16384) tokens = p.T > 65536 ? kMaxTokens : 16;
   int heads = p.c.H;
   const int64_t tiles = (p.T + tokens - 1) / tokens;
   // one token's heads in several workgroups where there are few tokens
@@ -234,8 +293,9 @@ hipError_t launch(const CacheRowsParams& p, hipStream_t st) {
   const int groups = (p.c.H + heads - 1) / heads;
   if (tiles * groups > kMaxGroups) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(tiles * groups));
-  if constexpr (WRITE) cache_write_kernel<T, Q8, VEC, LPR><<<grid, kThreads, 0, st>>>(p, tokens, heads, groups);
-  else cache_read_kernel<T, Q8, VEC, LPR><<<grid, kThreads, 0, st>>>(p, tokens, heads, groups);
+  const RowGrid g{tokens, heads, divisor((uint32_t)groups), divisor(2u * heads), __builtin_ctz((unsigned)p.c.P)};
+  if constexpr (WRITE) cache_write_kernel<T, Q8, VEC, LPR><<<grid, kThreads, 0, st>>>(p, g);
+  else cache_read_kernel<T, Q8, VEC, LPR><<<grid, kThreads, 0, st>>>(p, g);
   return hipGetLastError();
 }
 

@@ -11,15 +11,7 @@ __device__ __forceinline__ float q8_scale(unsigned amax) {
   return (a == a ? fmaxf(a, 1e-12f) : a) / 448.f;
 }
 
-// e4m3 bytes of x / scale, to nearest even.  Divided for: a product with the reciprocal may lie on the other
-// side of a value half way between two e4m3 values.
-__device__ __forceinline__ u32x2v q8_pack(const float (&x)[8], float scale) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = x[i] / scale;
-    v[i] = v[i] > 448.f ? 448.f : (v[i] < -448.f ? -448.f : v[i]);  // NaN passes
-  }
+__device__ __forceinline__ u32x2v q8_convert(const float (&v)[8]) {
   u32x2v r;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -27,6 +19,31 @@ __device__ __forceinline__ u32x2v q8_pack(const float (&x)[8], float scale) {
     r[h] = (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h + 2], v[4 * h + 3], w, true);
   }
   return r;
+}
+
+// e4m3 bytes of the quotients x / scale, to nearest even.  A product with the scale's reciprocal is off from the
+// quotient by less than 2^-21 of it, and may lie on the other side of a value half way between two e4m3 values: where
+// the products 2^-21 below and above it do not become the same bytes, in any of the wave's lanes, and for scales that
+// are not finite, the quotients are formed.  (8 divisions are 80 instructions, this is 40: 33 -> 22 us for 8192 tokens
+// of 8 heads of 128 columns.)  A product above 448 is so by less than 2^-20 of it, and becomes 448.
+__device__ __forceinline__ u32x2v q8_pack(const float (&x)[8], float scale) {
+  const float inv = __builtin_amdgcn_rcpf(scale);
+  float lo[8], hi[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = x[i] * inv;
+    lo[i] = y * (1.f - 0x1p-21f);
+    hi[i] = y * (1.f + 0x1p-21f);
+  }
+  const u32x2v q = q8_convert(lo), t = q8_convert(hi);
+  if (__ballot(!(scale < __builtin_inff()) || q[0] != t[0] || q[1] != t[1]) == 0) return q;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = x[i] / scale;
+    v[i] = v[i] > 448.f ? 448.f : (v[i] < -448.f ? -448.f : v[i]);  // NaN passes
+  }
+  return q8_convert(v);
 }
 
 __device__ __forceinline__ void q8_unpack(u32x2v w, float (&x)[8]) {
