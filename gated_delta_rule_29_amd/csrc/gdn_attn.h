@@ -99,7 +99,8 @@ struct AttnParams {
 struct AttnPlans {
   AttnPlan few, many;       // units 0: the class is empty.  fp32: all rows are in `few`
 };
-AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtype, bool q8, int64_t max_keys);
+// window: 0 leaves at least as many pieces as any.
+AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtype, bool q8, int64_t max_keys, int window);
 size_t attn_ws_bytes(const AttnPlans& pl, int Hk, int D);
 hipError_t launch_attn(AttnParams p, const AttnPlans& pl, int dtype, bool q8, void* ws, hipStream_t st);
 

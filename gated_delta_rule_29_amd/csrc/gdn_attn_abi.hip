@@ -128,8 +128,9 @@ int check_attn_rows(const gdn::Seqs& s, const int* cu_host, int G) {
 }
 
 gdn::AttnPlans plans(const gdn::Seqs& s, const int* cu_host, int Hq, int Hk, int D, int P, int width, int dtype,
-                     int cache_dtype) {
-  return gdn::attn_plans(cu_host, s.n, s.T, Hq / Hk, Hk, D, dtype, cache_dtype == GDN_DTYPE_E4M3, (int64_t)width * P);
+                     int cache_dtype, int window) {
+  return gdn::attn_plans(cu_host, s.n, s.T, Hq / Hk, Hk, D, dtype, cache_dtype == GDN_DTYPE_E4M3, (int64_t)width * P,
+                         window);
 }
 
 bool odd16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
@@ -152,7 +153,7 @@ int attn(const gdn::Seqs& s, const int* cu_host, const Attn& a, void* ws, size_t
   if (a.window < 0 || (a.window && !a.causal))
     return fail(GDN_ERR_INVALID, "window must be 0 or, in a causal call, positive (got %d)", a.window);
   GDN_TRY(check_attn_rows(s, cu_host, a.Hq / a.Hk));
-  const gdn::AttnPlans pl = plans(s, cu_host, a.Hq, a.Hk, a.D, a.P, a.width, a.dtype, a.cache_dtype);
+  const gdn::AttnPlans pl = plans(s, cu_host, a.Hq, a.Hk, a.D, a.P, a.width, a.dtype, a.cache_dtype, a.window);
   // (512 threads a workgroup at most, and two workgroups for 256 columns)
   for (const gdn::AttnPlan& q : {pl.few, pl.many})
     if (((int64_t)q.units + q.spare) * a.Hk > gdn::kMaxGroups / 4 ||
@@ -242,7 +243,7 @@ size_t paged_attn_workspace_bytes(int B, int T, int Hq, int Hk, int D, int P, in
                                   int cache_dtype) {
   gdn::Seqs s;
   if (dense(B, T, &s) || check_attn_sizes(Hq, Hk, D, P, max_pages, dtype) || check_attn_rows(s, nullptr, Hq / Hk)) return 0;
-  return gdn::attn_ws_bytes(plans(s, nullptr, Hq, Hk, D, P, max_pages, dtype, cache_dtype), Hk, D);
+  return gdn::attn_ws_bytes(plans(s, nullptr, Hq, Hk, D, P, max_pages, dtype, cache_dtype, 0), Hk, D);
 }
 
 size_t paged_attn_varlen_workspace_bytes(const int* cu_seqlens_host, int N, int Hq, int Hk, int D, int P,
@@ -251,7 +252,7 @@ size_t paged_attn_varlen_workspace_bytes(const int* cu_seqlens_host, int N, int 
   if (!cu_seqlens_host || N < 1 || packed(cu_seqlens_host, cu_seqlens_host, N, cu_seqlens_host[N], &s) ||
       check_attn_sizes(Hq, Hk, D, P, max_pages, dtype) || check_attn_rows(s, cu_seqlens_host, Hq / Hk))
     return 0;
-  return gdn::attn_ws_bytes(plans(s, cu_seqlens_host, Hq, Hk, D, P, max_pages, dtype, cache_dtype), Hk, D);
+  return gdn::attn_ws_bytes(plans(s, cu_seqlens_host, Hq, Hk, D, P, max_pages, dtype, cache_dtype, 0), Hk, D);
 }
 
 int paged_attn_fwd(const void* q, int64_t q_pitch, int64_t q_head, const void* k_cache, const void* v_cache,

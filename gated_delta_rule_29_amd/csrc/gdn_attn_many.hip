@@ -76,9 +76,8 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   constexpr int HV = D / DV;
   const int uh = blockIdx.x / HV, up = quotient(uh, p.by_heads);
   const int h = uh - up * p.Hk, c0 = blockIdx.x % HV * DV;  // c0: the first output column
-  const int id = p.plan.units + p.plan.spare - 1 - up;      // descending: a causal sequence's last rows see the most keys
   Unit u;
-  if (!find_unit<true>(p, id, lane, &u)) return;
+  if (!find_unit<true>(p, up, lane, &u)) return;
 
   const int row = u.row0 + kRows * wv + col;
   const bool live = row < u.row0 + u.nrows;

@@ -20,8 +20,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p, Divisor pe
   const int rest = quotient(blockIdx.x, p.by_heads), h = blockIdx.x - rest * p.Hk, id = quotient(rest, per_unit);
   Unit u;
   if (!find_unit<false>(p, id, lane, &u)) return;
-  const int pieces = min(u.pieces, 2 * p.plan.spare - u.slot);  // (fewer only with other offsets than the host's)
-  const int64_t step = (int64_t)p.Hk * p.plan.part_rows;  // rows from piece to piece
+  const int pieces = u.pieces;
+  const int64_t step = (int64_t)u.apart * p.Hk * p.plan.part_rows;  // rows from piece to piece
   const int first = (rest - id * (int)per_unit.by) * rows, end = min(first + rows, u.nrows);
   for (int at0 = first; at0 < end; at0 += RPW) {
     const int at = at0 + sub;
@@ -92,8 +92,10 @@ hipError_t join_width(const AttnParams& p, hipStream_t st) {
 }
 
 // Pieces beyond one a unit, so that a piece has about a `fill`-th of all keys of all heads' units.  least: tiles of
-// the sequence that has the fewest; if they are as many as the pieces, none is long enough to be cut.
-int spare_pieces(const AttnPlan& pl, int Hk, int64_t max_keys, int fill, int64_t least) {
+// the sequence that has the fewest; if they are as many as the pieces, none is long enough to be cut.  (A call that
+// cuts nothing has no join to launch, 5 to 9 us.)
+int spare_pieces(const AttnPlan& pl, int Hk, int64_t max_keys, int window, int fill, int64_t least) {
+  if (window && max_keys > (int64_t)window + pl.rows + 64) max_keys = (int64_t)window + pl.rows + 64;
   if (!pl.units || 2 * max_keys < 3 * pl.min_piece) return 0;
   const int spare = (fill + Hk - 1) / Hk;
   return least >= spare ? 0 : spare;
@@ -101,7 +103,8 @@ int spare_pieces(const AttnPlan& pl, int Hk, int64_t max_keys, int fill, int64_t
 
 }  // namespace
 
-AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtype, bool q8, int64_t max_keys) {
+AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtype, bool q8, int64_t max_keys,
+                     int window) {
   AttnPlans a{};
   const bool f32 = dtype == GDN_DTYPE_F32;
   const int64_t few_limit = f32 ? INT64_MAX : kFewRows;
@@ -136,13 +139,13 @@ AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtyp
   a.few.units = (int)(units_few < most ? units_few : most);
   a.few.part_rows = (int)(most_few < a.few.rows ? most_few : a.few.rows);
   a.few.min_piece = 512;
-  a.few.spare = spare_pieces(a.few, Hk, max_keys, 1024, least_few);
+  a.few.spare = spare_pieces(a.few, Hk, max_keys, window, 1024, least_few);
   a.many.rows = many;
   a.many.row_bits = __builtin_ctz((unsigned)many);
   a.many.units = (int)(units_many < most ? units_many : most);
   a.many.part_rows = (int)(most_many < many ? most_many : many);
   a.many.min_piece = 1024;
-  a.many.spare = spare_pieces(a.many, Hk, max_keys, 256, least_many);
+  a.many.spare = spare_pieces(a.many, Hk, max_keys, window, 256, least_many);
   return a;
 }
 
