@@ -264,3 +264,112 @@ def test_results_repeat():
     first = lib().paged_attn_step(q, *cache.args(), table, dl)
     for _ in range(5):
         assert torch.equal(first, lib().paged_attn_step(q, *cache.args(), table, dl))
+
+
+@pytest.mark.parametrize("D,kind", [(64, "same"), (64, "e4m3"), (128, "same"), (128, "e4m3"), (256, "same"),
+                                    (256, "e4m3")])
+def test_cut_chunks(D, kind):
+    """Chunks of several tiles over contexts that are cut into pieces: the first tiles of a chunk have fewer of them
+    than the last ones, and long chunks stand beside level ones and single tokens."""
+    check(26, [300, 1, 70, 3], [2900, 40, 4500, 10], 8, 2, D, 64, kind)
+    check(27, [700, 130], [0, 2200], 4, 1, D, 16, kind, how="odd", extra=100)
+    check(28, [90, 90], [3500, 3500], 4, 1, D, 32, kind, form="dense")
+    check(29, [40, 600], [5000, 1], 4, 2, D, 128, kind, causal=False)
+
+
+@pytest.mark.parametrize("window", [1, 33, 600, 4000])
+@pytest.mark.parametrize("D,kind", [(64, "same"), (128, "same"), (128, "e4m3"), (256, "same"), (256, "e4m3")])
+def test_windows_of_long_chunks(window, D, kind):
+    check(30, [400, 2, 50], [1500, 900, 5000], 8, 2, D, 32, kind, window=window)
+
+
+def test_fp32_chunks_that_are_cut():
+    check(31, [100, 1, 20], [2500, 700, 0], 4, 2, 128, 16, dtype="f32")
+    check(31, [100, 1, 20], [2500, 700, 0], 4, 2, 64, 16, "e4m3", dtype="f32", window=1800)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+def test_single_tokens_of_many_heads(D, kind):
+    """More query heads a key head than a tile of few rows has."""
+    check(32, [1, 1, 1], [1200, 0, 77], 66, 2, D, 16, kind, form="step")
+
+
+def test_many_long_sequences():
+    """More sequences than a wave has lanes, of both classes and both orders, cut."""
+    g = torch.Generator().manual_seed(33)
+    ctx = torch.randint(0, 400, (150,), generator=g).tolist()
+    new = [1 if i % 3 else 20 + i for i in range(150)]
+    ctx[3], ctx[77], ctx[148] = 3000, 4000, 5000
+    check(34, new, ctx, 4, 2, 64, 16)
+
+
+@pytest.mark.parametrize("D,kind", [(64, "same"), (128, "same"), (128, "e4m3"), (256, "same"), (256, "e4m3")])
+def test_not_finite_values_in_long_chunks(D, kind):
+    """NaN in values at many places of a long chunk, cut or not: each token's result has those that it sees, and
+    no other."""
+    g = torch.Generator().manual_seed(35)
+    new, L, Hq, Hk, P = 300, 2700, 4, 2, 32
+    for window in (0, 700):
+        cache = Cache(g, 90, Hk, P, D, kind)
+        table = pages_of(g, 90, [L], P)
+        q = queries(g, new, Hq, D, torch.bfloat16)
+        o, _, bound, _ = reference(q, cache, table, [L], [new], D ** -0.5, window=window)
+        # (column, place): before the window of all, of some, in the chunk, its last token's
+        places = [(0, 100), (1, L - new - 650), (2, L - new), (3, L - new + 63), (4, L - 130), (5, L - 1)]
+        for d, at in places:
+            page, place = int(table[0, at // P]), at % P
+            if kind == "e4m3":
+                cache.t["v"].view(torch.uint8)[page, :, place, d] = 0x7f
+            else:
+                cache.t["v"][page, :, place, d] = float("nan")
+        cu = torch.tensor([0, new], dtype=torch.int32)
+        got = lib().paged_attn_fwd_varlen(q[None], *cache.args(), table.to(DEV),
+                                          torch.tensor([L], dtype=torch.int32).to(DEV), cu.to(DEV), window=window,
+                                          **cache.scales())["o"][0].clone()
+        for d, at in places:
+            last = torch.arange(L - new, L)
+            sees = (last >= at) & ((last - at < window) if window else True)
+            bad = torch.isnan(got[:, :, d].float()).all(1).cpu()
+            none = torch.isnan(got[:, :, d].float()).any(1).cpu()
+            assert torch.equal(bad, sees) and torch.equal(none, sees), (d, at, window)
+            hit = sees.to(DEV)
+            got[hit, :, d] = 0
+            o[sees.numpy(), :, d] = 0
+        within("o", got, o, bound)
+
+
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+def test_pages_past_32_bits(kind):
+    """Pages whose elements lie past 2^32 of the cache."""
+    g = torch.Generator().manual_seed(36)
+    H, P, D, pages = 4, 64, 128, (1 << 32) // (4 * 64 * 128) + 80
+    lens, new = [1500, 300], [40, 1]
+    small = Cache(g, 40, H, P, D, kind)
+    table = pages_of(g, 40, lens, P)
+    big = {n: torch.empty(pages, H, P, D, dtype=small.t[n].dtype, device=DEV) for n in "kv"}
+    scales = {}
+    for n in "kv":
+        big[n][-40:] = small.t[n]
+        if kind == "e4m3":
+            scales[n + "_scale"] = torch.empty(pages, H, P, device=DEV)
+            scales[n + "_scale"][-40:] = small.s[n]
+    far = torch.where(table >= 0, table + pages - 40, table)
+    q = queries(g, 41, 8, D, torch.bfloat16)
+    dl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 40, 41], dtype=torch.int32)
+    a = lib().paged_attn_fwd_varlen(q[None], *small.args(), table.to(DEV), dl, cu.to(DEV), **small.scales())["o"]
+    b = lib().paged_attn_fwd_varlen(q[None], big["k"], big["v"], far.to(DEV), dl, cu.to(DEV), **scales)["o"]
+    assert torch.equal(a, b)
+    o, _, bound, _ = reference(q, small, table, lens, new, D ** -0.5)
+    within("o", a[0], o, bound)
+
+
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+def test_pages_that_sequences_share(kind):
+    """Sequences with a common beginning name the same pages; one names a page twice."""
+    def change(cache, table, lens):
+        table[1, :3] = table[0, :3]
+        table[2, 1] = table[2, 0]
+
+    check(37, [40, 1, 9], [50, 60, 30], 4, 2, 64, 16, kind, change=change)
