@@ -4,7 +4,9 @@
 //
 // All of it in fp32, on the fp32 16x16x4 matrix instructions (157 TFLOP/s at best, a sixteenth of bf16's, so
 // operands come straight from memory and the caches: keys as rows, values as columns).  A workgroup has a tile
-// of 16 or 32 rows, its four waves every fourth 16 keys each, as in the few-row kernel for bf16.
+// of 16 or 32 rows, its four waves every fourth 16 keys each, as in the few-row kernel for bf16.  Bound by the
+// latency of its loads: cross attention of 777, 5 and 130 tokens to 300, 1 and 77 states, 12 heads of 64 columns:
+// 26 us.
 #include "../../include/gdn.h"
 #include "gdn_attn_device.h"
 #include "gdn_q8.h"

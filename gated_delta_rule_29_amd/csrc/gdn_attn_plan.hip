@@ -138,8 +138,14 @@ AttnPlans attn_plans(const int* cu, int n, int T, int G, int Hk, int D, int dtyp
   const int64_t most = INT32_MAX / 2;
   a.few.units = (int)(units_few < most ? units_few : most);
   a.few.part_rows = (int)(most_few < a.few.rows ? most_few : a.few.rows);
+  // Pieces fill the chip once or twice.  Few rows, 256 / 512 / 1024 / 2048 pieces: one token after 131071 98 / 101 / 111 /
+  // 131 us, the same over 8 bits 58 / 52 / 59; 32 tokens after 0 .. 18600 241 / 227 / 221, over 8 bits 157 / 135 / 131;
+  // of 256 columns, 8 bits, 69 / 74 / 91.  Shortest piece 256 / 512 / 1024 keys: one token after 8191 18 / 16 / 20.
+  // Many rows, 256 / 384 / 512 pieces: 256 tokens after 32768 161 / 193 / 178, 2048 after 6000 235 / 241 / 305, 9 chunks
+  // of a serving step 122 / 114 / 123: pieces that are no whole number of rounds, and 128 KB written and read a
+  // piece, cost more than what they even out.
   a.few.min_piece = 512;
-  a.few.spare = spare_pieces(a.few, Hk, max_keys, window, 1024, least_few);
+  a.few.spare = spare_pieces(a.few, Hk, max_keys, window, 512, least_few);
   a.many.rows = many;
   a.many.row_bits = __builtin_ctz((unsigned)many);
   a.many.units = (int)(units_many < most ? units_many : most);

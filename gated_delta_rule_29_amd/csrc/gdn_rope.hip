@@ -9,7 +9,10 @@
 // quarter turn and a remainder of an eighth of a turn at most.
 //
 // A workgroup takes a few tokens: it forms their cosines and sines once, in LDS, and streams the heads
-// through them in 16-byte vectors.  Bound by memory.
+// through them in 16-byte vectors.  Bound by memory: 8192 tokens of 40 heads of 128 columns, bf16, 64 columns
+// turned: 27 us, 6.2 TB/s of what it reads and writes (partly in the last caches; 35 us call after call);
+// 16384 tokens of 18 heads of 256: 62 us, 4.9 TB/s, the rate of a large copy.  A token of 40 heads: 2.4 us, a chain
+// of three loads.
 #include "../../include/gdn.h"
 #include "gdn_attn.h"
 #include "gdn_layer_device.h"

@@ -42,7 +42,8 @@
  *    gdn_fwd_varlen_noalloc (one per GPU, held until the process ends).
  *  - Tensors are dense and row-major in the shapes given (no strides).  The layer operators
  *    take a pitch for their row inputs: the elements from one token's row to the next (at
- *    least the row's width), so that columns of a wider tensor are read in place.
+ *    least the row's width), so that columns of a wider tensor are read in place; the
+ *    full-attention layers' head tensors take one from head to head as well.
  *  - dtype: GDN_DTYPE_F32 (fp32 inputs, fp32 MFMA, fp32 state) or GDN_DTYPE_BF16 (bf16 q/k/v
  *    and bf16 outputs, bf16 MFMA operands, fp32 accumulation and fp32 state).  Gates (g, gk,
  *    beta), initial and final states are always fp32.  Gates are natural-log decays: a base-2
@@ -52,8 +53,8 @@
  *  - Every argument is validated on the host before anything is launched; on an error
  *    nothing is written.  The return value is a status code below, and gdn_last_error()
  *    returns a message for the calling thread's most recent failure.
- *  - Results are deterministic: no entry point uses atomics, so two identical calls give
- *    bitwise-identical outputs.
+ *  - Results are deterministic: no entry point uses atomics whose order could show (one builds
+ *    a bitmap in LDS with them), so two identical calls give bitwise-identical outputs.
  */
 #ifndef GDN_H_
 #define GDN_H_
@@ -861,7 +862,8 @@ GDN_API int rope_bwd(const void* dy, int64_t dy_pitch, int64_t dy_head_pitch, co
  * kv_cache_write -- rows of keys and values into their places of a cache.
  *   k, v [T, H, D] dtype;  slots [T] int32 (device): place slot % P of page slot / P.  A row whose slot is outside
  *   [0, pages * P) (a padded row) changes nothing, nor does a row that names the slot of an earlier
- *   row: the first row of a slot is the one that counts.
+ *   row: the first row of a slot is the one that counts (looked for among all earlier rows: time grows with the
+ *   square of T beyond some ten thousand rows).
  *   e4m3: scale = max(max |x|, 1e-12) / 448 over a token and head's D columns, values e4m3(x / scale) to
  *   nearest even.  A NaN makes its row's scale and values NaN.
  * Supported: D <= 512, H <= 4096.
