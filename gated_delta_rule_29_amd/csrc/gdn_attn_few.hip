@@ -10,8 +10,8 @@
 // under way while these are worked on.  The transposed scores' accumulators are the second product's operand
 // as they are: lane (lq, li) has keys 4 lq + r of each 16, for row li.
 //
-// One token after 131071 keys of 8 heads of 128 columns, bf16 (537 MB): 102 us and 7 for the join, 5.3 and 4.9 TB/s;
-// 32 single tokens over 8-bit caches (321 MB, contexts up to 20000): 62 + 5 us, 5.2 TB/s.  Page numbers are a load
+// One token after 131071 keys of 8 heads of 128 columns, bf16 (537 MB): 94 us, 5.7 TB/s, and 5 for the join; 32
+// single tokens over 8-bit caches (321 MB, contexts up to 20000): 66 + 5 us, 4.9 TB/s.  Page numbers are a load
 // before the loads: asked for a tile ahead they took 125 us to 113 and 89 to 71.
 #include "../../include/gdn.h"
 #include "gdn_attn_device.h"
