@@ -153,7 +153,9 @@ int attn(const gdn::Seqs& s, const int* cu_host, const Attn& a, void* ws, size_t
   if (a.window < 0 || (a.window && !a.causal))
     return fail(GDN_ERR_INVALID, "window must be 0 or, in a causal call, positive (got %d)", a.window);
   GDN_TRY(check_attn_rows(s, cu_host, a.Hq / a.Hk));
-  const gdn::AttnPlans pl = plans(s, cu_host, a.Hq, a.Hk, a.D, a.P, a.width, a.dtype, a.cache_dtype, a.window);
+  // A window of all keys that a sequence may have hides none; differences of positions and windows fit 32 bits.
+  const int window = a.window >= (int64_t)a.width * a.P ? 0 : a.window;
+  const gdn::AttnPlans pl = plans(s, cu_host, a.Hq, a.Hk, a.D, a.P, a.width, a.dtype, a.cache_dtype, window);
   // (512 threads a workgroup at most, and two workgroups for 256 columns)
   for (const gdn::AttnPlan& q : {pl.few, pl.many})
     if (((int64_t)q.units + q.spare) * a.Hk > gdn::kMaxGroups / 4 ||
@@ -170,7 +172,7 @@ int attn(const gdn::Seqs& s, const int* cu_host, const Attn& a, void* ws, size_t
   p.q_vec = !odd16(a.q) && a.q_pitch % 8 == 0 && a.q_head % 8 == 0;
   p.scale = a.scale * 1.4426950408889634f;
   p.causal = a.causal != 0;
-  p.window = a.window;
+  p.window = window;
   const hipError_t e = gdn::launch_attn(p, pl, a.dtype, q8, ws, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ok() : hip_fail(e, what);
 }

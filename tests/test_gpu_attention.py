@@ -373,3 +373,28 @@ def test_pages_that_sequences_share(kind):
         table[2, 1] = table[2, 0]
 
     check(37, [40, 1, 9], [50, 60, 30], 4, 2, 64, 16, kind, change=change)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_largest_window(dtype):
+    """A window of 2^31 - 1 hides nothing, also where a sequence's first tokens have no keys."""
+    g = torch.Generator().manual_seed(38)
+    t = TYPES[dtype]
+    new, lens = [1000, 5, 3], [100, 300, 1]
+    cache = Cache(g, 30, 2, 16, 64, "same", t)
+    table = pages_of(g, 30, lens, 16)
+    q = queries(g, sum(new), 4, 64, t)
+    cu = torch.tensor([0] + new).cumsum(0).to(torch.int32).to(DEV)
+    dl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    whole = lib().paged_attn_fwd_varlen(q[None], *cache.args(), table.to(DEV), dl, cu)["o"]
+    for window in (2 ** 31 - 1, 2 ** 30, 304, 303):
+        r = lib().paged_attn_fwd_varlen(q[None], *cache.args(), table.to(DEV), dl, cu, window=window)["o"]
+        assert torch.equal(r, whole), window
+    o, _, bound, _ = reference(q, cache, table, lens, new, 64 ** -0.5)
+    within("o", whole[0], o, bound)
+
+
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+def test_more_heads_of_a_key_head_than_a_tile_has_rows(kind):
+    check(39, [1, 3], [70, 1100], 300, 1, 64, 16, kind)
+    check(39, [1, 1], [70, 1100], 300, 1, 256, 16, kind, form="step")
