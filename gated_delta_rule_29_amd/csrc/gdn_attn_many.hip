@@ -253,22 +253,15 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
     constexpr bool EDGE = decltype(edge_t)::value;
     const int key = u.lo + TK * t;
     const float* scales = reinterpret_cast<const float*>(lds + 2 * M::STAGE + stage * M::SCALES) + sub * TK + 4 * half;
-    f32x16 z[2];  // (of one block of keys: even and odd steps, so that a product need not wait for the last one)
+    f32x16 z[KB];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) z[i][r] = 0.f;
-    if constexpr (KB == 2) {
+      for (int r = 0; r < 16; ++r) z[kb][r] = 0.f;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int s = 0; s < KS; ++s) z[kb] = mma32(key_rows(s, sub * M::KT + 32 * kb * RK), q[s], z[kb]);
-    } else {
-#pragma unroll
-      for (int s = 0; s < KS; ++s) z[s & 1] = mma32(key_rows(s, sub * M::KT), q[s], z[s & 1]);
-#pragma unroll
-      for (int r = 0; r < 16; ++r) z[0][r] += z[1][r];
-    }
+      for (int s = 0; s < KS; ++s) z[kb] = mma32(key_rows(s, sub * M::KT + 32 * kb * RK), q[s], z[kb]);
     if constexpr (!EDGE) {
       // four operands ahead of the products
       __builtin_amdgcn_sched_group_barrier(kDsRead, 4, 0);
