@@ -11,7 +11,7 @@
 // as they are: lane (lq, li) has keys 4 lq + r of each 16, for row li.
 //
 // One token after 131071 keys of 8 heads of 128 columns, bf16 (537 MB): 94 us, 5.7 TB/s, and 5 for the join; 32
-// single tokens over 8-bit caches (321 MB, contexts up to 20000): 66 + 5 us, 4.9 TB/s.  Page numbers are a load
+// single tokens over 8-bit caches (321 MB, contexts up to 20000): 67 + 5 us, 4.8 TB/s.  Page numbers are a load
 // before the loads: asked for a tile ahead they took 125 us to 113 and 89 to 71.
 #include "../../include/gdn.h"
 #include "gdn_attn_device.h"
@@ -215,7 +215,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnParams p) {
     }
     const bool part = key + kTile - 1 > all_last || key < all_first;  // not all rows see all keys
     const bool edge = part || key + kTile > u.hi;
-    bf16x8 pf[MT];
+    bf16x8 pf[MT], pl[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       float top = -__builtin_inff();
@@ -253,9 +253,27 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnParams p) {
           if constexpr (Q8) e[kt][r] = edge && z[mt][kt][r] == -__builtin_inff() ? 0.f : e[kt][r] * vs[kt][r];
         }
       }
-      // Weights enter the product as bf16: each is off by 2^-8 of itself at most, in either direction, where
-      // the output's own rounding is as large.
-      pf[mt] = pack8<bf16>(e[0], e[1]);
+      // Weights enter the product as two bf16: the upper bits, and what is left, rounded: off by 2^-16 of itself at
+      // most.  (As one they are off by 2^-8, as much as the output's own rounding; the times are the same, 100 us for
+      // one token after 131071, 75 for 32 over 8 bits.)
+      u32x4v upper;
+      f32x4 left[2];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x = e[kt][r], up = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+          left[kt][r] = x - up;
+          // (an infinite scale)
+          if constexpr (Q8) left[kt][r] = __builtin_fabsf(x) == __builtin_inff() ? 0.f : left[kt][r];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          upper[2 * kt + i] =
+              __builtin_amdgcn_perm(__float_as_uint(e[kt][2 * i + 1]), __float_as_uint(e[kt][2 * i]), 0x07060302u);
+      }
+      pf[mt] = __builtin_bit_cast(bf16x8, upper);
+      pl[mt] = pack8<bf16>(left[0], left[1]);
     }
     const uint32_t tr = tr0 + stage * kTile * RB;
     auto values = [&](int b) {
@@ -276,7 +294,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnParams p) {
       for (int b = 0; b < DB; ++b) {
         const bf16x8 v = values(b);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) o[mt][b] = mma16(v, pf[mt], o[mt][b]);
+        for (int mt = 0; mt < MT; ++mt) o[mt][b] = mma16(v, pl[mt], mma16(v, pf[mt], o[mt][b]));
       }
     } else {
       // a product with a weight of 0 would not be 0: such values are added where they are seen, and taken out
@@ -301,7 +319,7 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnParams p) {
       for (int b = 0; b < DB; ++b) {
         const bf16x8 v = finite_part(values(b));
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) o[mt][b] = mma16(v, pf[mt], o[mt][b]);
+        for (int mt = 0; mt < MT; ++mt) o[mt][b] = mma16(v, pl[mt], mma16(v, pf[mt], o[mt][b]));
         __builtin_amdgcn_sched_barrier(0);  // (rare: few registers before speed)
       }
     }
