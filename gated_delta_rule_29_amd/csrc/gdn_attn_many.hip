@@ -315,8 +315,14 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
           // (a hidden key's scale may be anything)
           if constexpr (Q8) e = EDGE && x == -__builtin_inff() ? 0.f : e * vs[r];
           // Weights enter the product as bf16: each is off by 2^-8 of itself at most, in either direction,
-          // where the output's own rounding is as large.
-          pf[2 * kb + g / 2][4 * (g & 1) + r] = (bf16)e;
+          // where the output's own rounding is as large.  At the edges, where rows may see a few keys only, what the
+          // rounding leaves follows in a product of its own (2% of a serving step's chunks, nothing of a long prompt).
+          const bf16 w = (bf16)e;
+          pf[2 * kb + g / 2][4 * (g & 1) + r] = w;
+          if constexpr (EDGE) {
+            z[kb][4 * g + r] = e - (float)w;
+            if constexpr (Q8) z[kb][4 * g + r] = __builtin_fabsf((float)w) == __builtin_inff() ? 0.f : z[kb][4 * g + r];
+          }
         }
       }
     auto values = [&](int s, int b) {
@@ -338,6 +344,16 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
     for (int s = 0; s < PS; ++s)
 #pragma unroll
       for (int b = 0; b < DB; ++b) o[b] = mma32(values(s, b), pf[s], o[b]);
+    if constexpr (EDGE) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < PS; ++s) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) pf[s][j] = (bf16)z[s / 2][8 * (s & 1) + j];
+#pragma unroll
+        for (int b = 0; b < DB; ++b) o[b] = mma32(values(s, b), pf[s], o[b]);
+      }
+    }
     if constexpr (!EDGE) {
       __builtin_amdgcn_sched_group_barrier(kDsRead, Q8 ? 6 : 4, 1);
       __builtin_amdgcn_sched_group_barrier(kValu, Q8 ? 32 : 24, 1);

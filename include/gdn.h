@@ -838,8 +838,8 @@ GDN_API int rms_norm_bwd(const void* dy, int64_t dy_pitch, const void* s, int64_
  *    k_scale, v_scale [pages, Hk, P] fp32 (NULL otherwise): a row stands for its values times its scale.  P, the
  *    places of a page, is 16, 32, .. or 1024 (GDN_ERR_UNSUPPORTED otherwise); pages * P < 2^31.
  *  - scores, softmax statistics and sums are fp32, each result is rounded once; with bf16 activations the
- *    softmax's weights enter the product with the values as bf16 where a sequence and key head has more than 32 rows
- *    (tokens times query heads), as the sum of two bf16 otherwise.  Results are deterministic.
+ *    softmax's weights enter the product with the values as the sum of two bf16, and as one where a sequence
+ *    and key head has more than 32 rows (tokens times query heads) and all rows of 32 see the key.  Results are deterministic.
  * ------------------------------------------------------------------------------------------ */
 
 /*
