@@ -210,6 +210,14 @@ def kv_cache_read(k_cache, v_cache, slots, k_scale=None, v_scale=None, *, dtype=
 
 # --------------------------------------------------------------------------------------- attention
 
+def _window(n):
+    """A window as the library's 32-bit integer: a larger one hides no more than the largest, nothing (ctypes would
+    pass on its low bits)."""
+    if n < 0:
+        raise ValueError("window must not be negative, got %r" % (n,))
+    return n if n <= _INT else _INT
+
+
 def _attn_args(q, n, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, scale):
     """The arguments that the forms share: of n sequences, up to the scale; and the sizes."""
     dev, dt, code = _act(q, "q", q.dim())
@@ -263,7 +271,7 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, k_scale=None, v_s
     lse = torch.empty(B, T, Hq, dtype=F32, device=dev) if want_lse else None
     n = _lib.load().paged_attn_workspace_bytes(B, T, *ws_sizes)
     ws = _workspace(n, dev)
-    _call("paged_attn_fwd", dev, *args, scale, 1 if causal else 0, window, o.data_ptr(),
+    _call("paged_attn_fwd", dev, *args, scale, 1 if causal else 0, _window(window), o.data_ptr(),
           lse.data_ptr() if want_lse else None, B, T, *sizes, ws.data_ptr() if n else None, n)
     return {"o": o, "lse": lse} if want_lse else {"o": o}
 
@@ -294,8 +302,8 @@ def paged_attn_fwd_varlen(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens
     lse = torch.empty(1, T, Hq, dtype=F32, device=dev) if want_lse else None
     n = _lib.load().paged_attn_varlen_workspace_bytes(host.data_ptr(), N, *ws_sizes)
     ws = _workspace(n, dev)
-    _call("paged_attn_fwd_varlen", dev, *args, cu.data_ptr(), host.data_ptr(), N, scale, 1 if causal else 0, window,
-          o.data_ptr(), lse.data_ptr() if want_lse else None, T, *sizes, ws.data_ptr() if n else None, n)
+    _call("paged_attn_fwd_varlen", dev, *args, cu.data_ptr(), host.data_ptr(), N, scale, 1 if causal else 0,
+          _window(window), o.data_ptr(), lse.data_ptr() if want_lse else None, T, *sizes, ws.data_ptr() if n else None, n)
     return {"o": o, "lse": lse} if want_lse else {"o": o}
 
 
@@ -312,5 +320,5 @@ def paged_attn_step(q, k_cache, v_cache, block_table, seq_lens, k_scale=None, v_
     o = _like(q)
     n = _lib.load().paged_attn_workspace_bytes(B, 1, *ws_sizes)
     ws = _workspace(n, dev)
-    _call("paged_attn_step", dev, *args, scale, window, o.data_ptr(), B, *sizes, ws.data_ptr() if n else None, n)
+    _call("paged_attn_step", dev, *args, scale, _window(window), o.data_ptr(), B, *sizes, ws.data_ptr() if n else None, n)
     return o
