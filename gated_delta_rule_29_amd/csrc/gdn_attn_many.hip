@@ -245,7 +245,8 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
 
   // Maxima are kept while a new one is less than 2^8 times the old one's weight: outputs and sum are then as
   // exact, and most tiles change nothing.
-  const float slack = 8.f / p.scale;
+  // (Finite for the smallest scales, too: a sum of infinities of both signs would compare as false for ever.)
+  const float slack = fminf(8.f / p.scale, 0x1.fffffep127f);
 
   auto key_rows = [&](int s, int off) { return read16((KP == 1 ? kp[0] ^ (32 * s) : kp[s % KP]) + off); };
   // One tile, number t, the stage's number `sub`.  EDGE: some of its keys are not seen by some of the wave's rows.
