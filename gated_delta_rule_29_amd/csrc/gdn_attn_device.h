@@ -198,6 +198,14 @@ __device__ __forceinline__ bf16x8 finite_part(const bf16x8& v) {
   for (int i = 0; i < 8; ++i) b[i] = (b[i] & 0x7f80) == 0x7f80 ? 0 : b[i];
   return __builtin_bit_cast(bf16x8, b);
 }
+// A weight w of a bf16 cache's values as two bf16, upper (exact in bf16, as fp32 bits) and what is left, which is
+// rounded to bf16: off by 2^-16 of w at most.  From w = 2^-102 on both are positive (upper is cut from the number below
+// w, so that something is left of 1, too, which the key of a row's maximum has): products of 0, or of both signs, with
+// an infinite value that is seen would make its column NaN.
+__device__ __forceinline__ unsigned upper_bf16(float w) {
+  const unsigned b = __float_as_uint(w);
+  return (max(b, 1u) - 1u) & 0xffff0000u;
+}
 // Weight of a partial result whose maximum is m in a whole whose maximum is top (both may be -infinity).
 __device__ __forceinline__ float part_weight(float m, float top) {
   return m == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(m - top);

@@ -254,23 +254,25 @@ __global__ __launch_bounds__(256) void attn_few_kernel(AttnParams p) {
         }
       }
       // Weights enter the product as two bf16: the upper bits, and what is left, rounded: off by 2^-16 of itself at
-      // most.  (As one they are off by 2^-8, as much as the output's own rounding; the times are the same, 100 us for
+      // most.  (As one they are off by 2^-8, as much as the output's own rounding; the times are the same, 101 us for
       // one token after 131071, 75 for 32 over 8 bits.)
       u32x4v upper;
       f32x4 left[2];
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
+        unsigned up[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float x = e[kt][r], up = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-          left[kt][r] = x - up;
+          const float x = e[kt][r];
+          // (8-bit values are finite or NaN, and their weights of either sign)
+          if constexpr (Q8) up[r] = __float_as_uint(x) & 0xffff0000u;
+          else up[r] = upper_bf16(x);
+          left[kt][r] = x - __uint_as_float(up[r]);
           // (an infinite scale)
           if constexpr (Q8) left[kt][r] = __builtin_fabsf(x) == __builtin_inff() ? 0.f : left[kt][r];
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          upper[2 * kt + i] =
-              __builtin_amdgcn_perm(__float_as_uint(e[kt][2 * i + 1]), __float_as_uint(e[kt][2 * i]), 0x07060302u);
+        for (int i = 0; i < 2; ++i) upper[2 * kt + i] = __builtin_amdgcn_perm(up[2 * i + 1], up[2 * i], 0x07060302u);
       }
       pf[mt] = __builtin_bit_cast(bf16x8, upper);
       pl[mt] = pack8<bf16>(left[0], left[1]);

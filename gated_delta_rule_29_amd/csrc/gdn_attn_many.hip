@@ -318,7 +318,9 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
           // Weights enter the product as bf16: each is off by 2^-8 of itself at most, in either direction,
           // where the output's own rounding is as large.  At the edges, where rows may see a few keys only, what the
           // rounding leaves follows in a product of its own (2% of a serving step's chunks, nothing of a long prompt).
-          const bf16 w = (bf16)e;
+          bf16 w = (bf16)e;
+          // (8-bit values are finite or NaN, and their weights of either sign)
+          if constexpr (EDGE && !Q8) w = __builtin_bit_cast(bf16, (unsigned short)(upper_bf16(e) >> 16));
           pf[2 * kb + g / 2][4 * (g & 1) + r] = w;
           if constexpr (EDGE) {
             z[kb][4 * g + r] = e - (float)w;
