@@ -435,7 +435,6 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
         if constexpr (Q8) x *= p.ks[place];
         float weight = __builtin_amdgcn_exp2f(__builtin_fmaf(x, p.scale, off));
         if constexpr (Q8) weight *= p.vs[place];
-        weight = (float)(bf16)weight;
         const bool seen = (unsigned)(key - first) < seen_n;
 #pragma unroll
         for (int b = 0; b < DB; ++b)

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.attention_util import DEV, TYPES, Cache, pages_of, reference, within
+from tests.attention_util import DEV, TYPES, U, Cache, pages_of, reference, within
 from tests.test_gpu_attention import KINDS, check, lib
 
 pytestmark = pytest.mark.gpu
@@ -53,5 +53,58 @@ def test_infinite_values_that_tokens_see(D, dtype):
             t0 += new[i]
         print("  case", new, ctx, window, D, dtype, flush=True)
         r = _call(q, cache, table, lens, new, window)
+        within("o", r["o"][0], o, bound)
+        within("lse", r["lse"][0], lse, lbound)
+
+
+def _cancelling(seed, kind, D, Hq, Hk, lens, new, dtype="bf16"):
+    """Every other key has weight 1 and values of 1, the others weight e^-a and values of about -e^c, with a of the token
+    and head and c of the column: results are small beside the sum of their terms' sizes, so that a relative error of the
+    weights e^-a, which a rounding to bf16 takes no two of alike, shows in them as it is."""
+    g = torch.Generator().manual_seed(seed)
+    P = 16
+    pages = sum(-(-n // P) for n in lens) + 1
+    cache = Cache(g, pages, Hk, P, D, kind, TYPES[dtype])
+    k, v = torch.zeros(pages, Hk, P, D), torch.ones(pages, Hk, P, D)
+    k[:, :, 1::2, 0] = -1.0
+    v[:, :, 1::2] = -torch.exp(3 * torch.rand(D, generator=g))
+    cache.put("k", k, TYPES[dtype])
+    cache.put("v", v, TYPES[dtype])
+    q = torch.zeros(sum(new), Hq, D)
+    q[:, :, 0] = 0.05 + 2.95 * torch.rand(sum(new), Hq, generator=g)
+    return q.to(TYPES[dtype]).to(DEV), cache, pages_of(g, pages, lens, P)
+
+
+def _two_bf16(q, cache, table, lens, new):
+    """The oracle and its bound where weights enter as two bf16: the first is off by less than 2^-7 of the weight's power
+    of two, the second rounds that to 2^-9 of it, so a weight is off by 2^-16 of itself at most; the sums as in
+    attention_util, and two roundings more for weights times 8-bit rows' scales."""
+    o, lse, bound, lbound = reference(q, cache, table, lens, new, 1.0)
+    # (|v| is 1 or more in every place, so that the weighted mean of |v| is taken from the oracle on |v|)
+    size = {n: np.abs(x) if n == "v" else x for n, x in cache.values.items()}
+    keep, cache.values = cache.values, size
+    mean = reference(q, cache, table, lens, new, 1.0)[0]
+    cache.values = keep
+    L, D = max(lens), q.shape[-1]
+    d = (D + 4) * U * 3.0 + (8 + 2 * L) * U  # (scores are 3 at most)
+    return o, lse, (2 * d + 2.0 ** -16) * mean, lbound
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
+def test_weights_beside_values_that_are_not_finite(D, kind):
+    """NaN in a place that only a chunk's last token sees: the others' weights enter as exactly as without it."""
+    for seed, Hq, Hk, new, lens in ((80, 2, 2, [60], [60]), (81, 8, 2, [40], [63]), (82, 4, 1, [6], [40])):
+        q, cache, table = _cancelling(seed, kind, D, Hq, Hk, lens, new)
+        o, lse, bound, lbound = _two_bf16(q, cache, table, lens, new)
+        last, d = lens[0] - 1, D - 3
+        page, place = int(table[0, last // 16]), last % 16
+        if kind == "e4m3":
+            cache.t["v"].view(torch.uint8)[page, :, place, d] = 0x7f
+        else:
+            cache.t["v"][page, :, place, d] = float("nan")
+        o[-1, :, d] = np.nan
+        print("  case", new, lens, Hq, Hk, D, kind, flush=True)
+        r = _call(q, cache, table, lens, new, scale=1.0)
         within("o", r["o"][0], o, bound)
         within("lse", r["lse"][0], lse, lbound)
