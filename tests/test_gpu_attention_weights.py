@@ -92,6 +92,20 @@ def _two_bf16(q, cache, table, lens, new):
 
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("kind", ["same", "e4m3"])
+def test_weights_are_two_bf16(D, kind):
+    """Few rows, cut or not, and tiles of many rows whose keys some rows see in part (all of them here)."""
+    for seed, Hq, Hk, new, lens in ((70, 6, 2, [1, 1, 1], [100, 33, 1]), (71, 4, 1, [4, 8, 1], [64, 300, 3000]),
+                                    (72, 2, 2, [60, 40], [60, 50]), (73, 8, 2, [40, 1], [63, 5])):
+        q, cache, table = _cancelling(seed, kind, D, Hq, Hk, lens, new)
+        o, lse, bound, lbound = _two_bf16(q, cache, table, lens, new)
+        print("  case", new, lens, Hq, Hk, D, kind, flush=True)
+        r = _call(q, cache, table, lens, new, scale=1.0)
+        within("o", r["o"][0], o, bound)
+        within("lse", r["lse"][0], lse, lbound)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["same", "e4m3"])
 def test_weights_beside_values_that_are_not_finite(D, kind):
     """NaN in a place that only a chunk's last token sees: the others' weights enter as exactly as without it."""
     for seed, Hq, Hk, new, lens in ((80, 2, 2, [60], [60]), (81, 8, 2, [40], [63]), (82, 4, 1, [6], [40])):
