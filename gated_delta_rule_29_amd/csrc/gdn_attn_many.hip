@@ -68,7 +68,7 @@ struct Many {
   static constexpr int LDS = 2 * (STAGE + SCALES);
 };
 
-template <bool Q8, int D, int NW>
+template <bool Q8, int D, int NW, bool LSE>
 __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   using M = Many<Q8, D, NW>;
   constexpr int RK = M::RK, RV = M::RV, DV = M::DV, CB = Q8 ? D : 2 * D, VB = Q8 ? DV : 2 * DV;  // CB, VB: in the cache
@@ -116,7 +116,14 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   for (int b = 0; b < DB; ++b)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[b][r] = 0.f;
-  float m = -__builtin_inff(), l = 0.f;  // the maximum is of products, before the scale
+  float m = -__builtin_inff();  // of products, before the scale
+  // l, which outputs are divided by, sums the weights as they enter the product: an error that all terms of a result
+  // share drops out, and a row that one key dominates gets that key's value, whatever its weight (with the weights
+  // before their rounding it was off by up to 2^-8, the same in every column).  8-bit rows enter with their scale, of
+  // which a sum of weights has no part.  le sums the weights themselves, for lse: both take 1420 us where one takes 1400
+  // (8192 tokens after 8192), so calls without lse leave it out.
+  constexpr bool AS_THEY_ENTER = !Q8;
+  float l = 0.f, le = 0.f;
 
   const uint32_t base = dma::lds_addr(lds);
   // where a stage's operands are read; the other stage is `hop` away
@@ -243,8 +250,9 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   // few) are left out and added in the end, key by key.
   unsigned long long odd = 0;
 
-  // Maxima are kept while a new one is less than 2^8 times the old one's weight: outputs and sum are then as
-  // exact, and most tiles change nothing.
+  // Maxima are kept while a new one is less than 2^8 times the old one's weight: most tiles change nothing.  fp32 sums
+  // and the weights' relative roundings are as exact with weights up to 2^8; only the largest weight, which would be 1,
+  // is rounded as the others are.
   // (Finite for the smallest scales, too: a sum of infinities of both signs would compare as false for ever.)
   const float slack = fminf(8.f / p.scale, 0x1.fffffep127f);
 
@@ -296,6 +304,7 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
       const float now = fmaxf(m, top), a = part_weight(m * p.scale, now * p.scale);
       m = now;
       l *= a;
+      if constexpr (LSE) le *= a;
 #pragma unroll
       for (int b = 0; b < DB; ++b) o[b] *= a;
     }
@@ -312,7 +321,8 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
         for (int r = 0; r < 4; ++r) {
           const float x = z[kb][4 * g + r];
           float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x, p.scale, off));
-          l += e;
+          if constexpr (EDGE || !AS_THEY_ENTER) l += e;
+          if constexpr (LSE) le += e;
           // (a hidden key's scale may be anything)
           if constexpr (Q8) e = EDGE && x == -__builtin_inff() ? 0.f : e * vs[r];
           // Weights enter the product as bf16: each is off by 2^-8 of itself at most, in either direction,
@@ -328,6 +338,14 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
           }
         }
       }
+    if constexpr (!EDGE && AS_THEY_ENTER) {
+      typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+      const bf16x2 one = {(bf16)1.f, (bf16)1.f};
+#pragma unroll
+      for (int s = 0; s < PS; ++s)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pf[s][j], pf[s][j + 1]}, one, l, false);
+    }
     auto values = [&](int s, int b) {
       const int x = VP == 1 ? 64 * b : 0, off = sub * M::VT + 16 * s * RV;
       const u32x2v lo = tr16((vp[0][b % VP] ^ x) + off), hi = tr16((vp[1][b % VP] ^ x) + off);
@@ -458,6 +476,7 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
   m *= p.scale;
 
   l = add_halves(l);
+  if constexpr (LSE) le = add_halves(le);
   if (!live) return;
   // lane: columns 32 b + 8 g + 4 half + r of its row
   if (u.pieces == 1) {
@@ -471,21 +490,23 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
         const float r[4] = {o[b][4 * g] * inv, o[b][4 * g + 1] * inv, o[b][4 * g + 2] * inv, o[b][4 * g + 3] * inv};
         storev<bf16, 4>(out + 32 * b + 8 * g, r);
       }
-    if (p.lse && half == 0 && c0 == 0) p.lse[to] = row_lse(m, l);
+    if (p.lse && half == 0 && c0 == 0) p.lse[to] = row_lse(m, LSE ? le : l);
   } else {
     const int at = row - u.row0;
+    // (one sum a piece: outputs are scaled to it)
+    const float f = !LSE || l == 0.f ? 1.f : le / l;
     float* out = part_outputs(p, u.slot, h) + (int64_t)at * D + c0 + 4 * half;
 #pragma unroll
     for (int b = 0; b < DB; ++b)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const float r[4] = {o[b][4 * g], o[b][4 * g + 1], o[b][4 * g + 2], o[b][4 * g + 3]};
+        const float r[4] = {o[b][4 * g] * f, o[b][4 * g + 1] * f, o[b][4 * g + 2] * f, o[b][4 * g + 3] * f};
         storev<float, 4>(out + 32 * b + 8 * g, r);
       }
     if (half == 0 && c0 == 0) {
       float* s = part_sums(p, u.slot, h) + 2 * at;
       s[0] = m;
-      s[1] = l;
+      s[1] = LSE ? le : l;
     }
   }
 }
@@ -494,7 +515,8 @@ template <bool Q8, int D>
 hipError_t launch(const AttnParams& p, hipStream_t st) {
   constexpr int NW = many_rows(D, Q8) / kRows;
   const int64_t groups = ((int64_t)p.plan.units + p.plan.spare) * p.Hk * (D / Many<Q8, D, NW>::DV);
-  attn_many_kernel<Q8, D, NW><<<dim3((unsigned)groups), 64 * NW, 0, st>>>(p);
+  if (!Q8 && p.lse) attn_many_kernel<Q8, D, NW, !Q8><<<dim3((unsigned)groups), 64 * NW, 0, st>>>(p);
+  else attn_many_kernel<Q8, D, NW, false><<<dim3((unsigned)groups), 64 * NW, 0, st>>>(p);
   return hipGetLastError();
 }
 

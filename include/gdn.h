@@ -839,7 +839,9 @@ GDN_API int rms_norm_bwd(const void* dy, int64_t dy_pitch, const void* s, int64_
  *    places of a page, is 16, 32, .. or 1024 (GDN_ERR_UNSUPPORTED otherwise); pages * P < 2^31.
  *  - scores, softmax statistics and sums are fp32, each result is rounded once; with bf16 activations the
  *    softmax's weights enter the product with the values as the sum of two bf16, and as one where a sequence
- *    and key head has more than 32 rows (tokens times query heads) and all rows of 32 see the key.  Results are deterministic.
+ *    and key head has more than 32 rows (tokens times query heads) and all rows of 32 see the key.  With a bf16 cache
+ *    the sum that results are divided by is of those weights, so that what all terms of a result share drops out; lse is
+ *    of the weights in fp32.  Results are deterministic.
  * ------------------------------------------------------------------------------------------ */
 
 /*

@@ -122,3 +122,46 @@ def test_weights_beside_values_that_are_not_finite(D, kind):
         r = _call(q, cache, table, lens, new, scale=1.0)
         within("o", r["o"][0], o, bound)
         within("lse", r["lse"][0], lse, lbound)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("want_lse", [False, True])
+def test_rows_that_one_key_dominates(D, want_lse):
+    """A key in a tile that all rows see has e^3 to e^5.4 of the weight of the row's first maximum, all others next to
+    nothing.  Weights w_j (1 + d_j), |d_j| <= 2^-8, in products and sum alike move a result by
+    sum w_j d_j (v_j - o) / sum w_j (1 + d_j): by 2^-8 / (1 - 2^-8) of the weighted mean of |v_j - o| at most, which is
+    small where one key has nearly all of the weight.  (Not so of 8-bit rows, whose weights enter with their scale.)"""
+    g = torch.Generator().manual_seed(90)
+    Hq, Hk, P = 4, 2, 16
+    for new, lens in (([40, 1], [1100, 700]), ([64], [5000])):
+        pages = sum(-(-n // P) for n in lens) + 1
+        cache = Cache(g, pages, Hk, P, D, "same")
+        table = pages_of(g, pages, lens, P)
+        k = torch.zeros(pages, Hk, P, D)
+        k[..., 0] = -16.0
+        for i in range(len(lens)):
+            k[int(table[i, 0]), :, 3] = 0.0
+            k[int(table[i, 200 // P]), :, 200 % P, 0] = 1.0
+        cache.put("k", k, torch.bfloat16)
+        q = torch.zeros(sum(new), Hq, D)
+        q[:, :, 0] = 3 + 2.4 * torch.rand(sum(new), Hq, generator=g)
+        q = q.to(torch.bfloat16).to(DEV)
+        o, lse, _, lbound = reference(q, cache, table, lens, new, 1.0)
+        a = q[:, :, :1].double().cpu().numpy()
+        bound, t0 = np.zeros_like(o), 0
+        for i, n in enumerate(new):
+            first, main = (np.repeat(cache.values["v"][int(table[i, at // P]), :, at % P], Hq // Hk, 0) for at in (3, 200))
+            x = a[t0:t0 + n]
+            r = o[t0:t0 + n]
+            spread = (np.exp(x) * np.abs(main - r) + np.abs(first - r)) / (np.exp(x) + 1)
+            mean = (np.exp(x) * np.abs(main) + np.abs(first)) / (np.exp(x) + 1)
+            # (the two keys' scores are below 6, and the others' weights, e^-48 each, within the sums' roundings)
+            bound[t0:t0 + n] = 2.0 ** -8 / (1 - 2.0 ** -8) * spread + 2 * ((D + 4) * U * 6 + (4 + 2 * lens[i]) * U) * mean
+            t0 += n
+        cu = torch.tensor([0] + new).cumsum(0).to(torch.int32)
+        print("  case", new, lens, D, want_lse, flush=True)
+        r = lib().paged_attn_fwd_varlen(q[None], *cache.args(), table.to(DEV), torch.tensor(lens, dtype=torch.int32).to(DEV),
+                                        cu.to(DEV), scale=1.0, want_lse=want_lse, cu_seqlens_host=cu)
+        within("o", r["o"][0], o, bound)
+        if want_lse:
+            within("lse", r["lse"][0], lse, lbound)
