@@ -69,7 +69,11 @@ struct AttnPlan {
 };
 
 // A call's sequences fall into two classes: with at most kFewRows rows (each wave takes its own keys) and
-// with more (each wave takes its own rows).
+// with more (each wave takes its own rows).  A sequence after 32768 keys, 8 key heads of 128 columns, us as few / as
+// many: 17 rows 43 / 39 over bf16 and 43 / 54 over 8 bits, 32 rows 45 / 39 and 44 / 54, 40 rows 58 / 40 and 63 / 54, 64
+// rows 60 / 40 and 63 / 56; eight of them: 32 rows 209 / 188 and 177 / 276, 40 rows 275 / 188 and 320 / 281; eight after
+// 1000 keys: 32 rows 26 / 24 and 25 / 39, 40 rows 32 / 24 and 32 / 40.  (17 to 32 rows over bf16 keep the class
+// whose weights are two bf16, for a tenth of their time.)
 constexpr int kFewRows = 32;
 // Rows of a tile of the second class.  256 bf16 columns take twice the registers: one wave a SIMD instead of two.
 constexpr int many_rows(int D, bool q8) { return D == 256 && !q8 ? 128 : 256; }

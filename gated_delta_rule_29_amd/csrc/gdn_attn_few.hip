@@ -12,7 +12,9 @@
 //
 // One token after 131071 keys of 8 heads of 128 columns, bf16 (537 MB): 94 us, 5.7 TB/s, and 5 for the join; 32
 // single tokens over 8-bit caches (321 MB, contexts up to 20000): 67 + 5 us, 4.8 TB/s.  Page numbers are a load
-// before the loads: asked for a tile ahead they took 125 us to 113 and 89 to 71.
+// before the loads: asked for a tile ahead they took 125 us to 113 and 89 to 71.  Of 256 columns, 16 query and 2 key
+// heads, which leave one wave a SIMD: one token after 131071 62 us (268 MB, 4.3 TB/s), over 8 bits 53 (136 MB, 2.6
+// TB/s); 32 single tokens after 0 .. 18600 121 us (610 MB, 5 TB/s), over 8 bits 77 (310 MB, 4 TB/s).
 #include "../../include/gdn.h"
 #include "gdn_attn_device.h"
 #include "gdn_q8.h"

@@ -11,10 +11,10 @@
 //
 // 8192 tokens after 8192, 32 query and 8 key heads of 128 columns, bf16: 1370 to 1450 us by the card's clock,
 // 1.14 to 1.2 PFLOP/s of the keys that are seen, where a large library product reaches 1.21.  Bound by instruction
-// issue: a tile of 64 keys is 32 products of 32 cycles and some 180 vector instructions a wave, and a product keeps
-// the other wave's from issuing for about half of its time; matrix units are busy 61% of the time.
-// Of 4096 tokens after 4096 (TFLOP/s): 128 columns over 8 bits 735; 64 columns 850, over 8 bits 690; 256 columns
-// 700 to 750, over 8 bits 510.  Tiles of 128 rows of four waves, two groups of waves that take turns at products and
+// issue: a tile of 64 keys is 32 products of 32 cycles and some 140 other vector instructions a wave, and a product keeps
+// the other wave's from issuing for about half of its time; matrix units are busy 59 to 61% of the time.
+// Of 4096 tokens after 4096 (TFLOP/s): 128 columns over 8 bits 735 (two multiplications more for each score, 5 registers in
+// scratch, and one tile a stage); 64 columns 850, over 8 bits 690; 256 columns 700 to 750, over 8 bits 510.  Tiles of 128 rows of four waves, two groups of waves that take turns at products and
 // exponentials (1552 us), and both interleaved by hand in a wave (1621) were no faster.
 #include "../../include/gdn.h"
 #include "gdn_attn_device.h"
@@ -54,8 +54,9 @@ __device__ __forceinline__ int swz(int row) {
 template <bool Q8, int D, int NW>
 struct Many {
   // Output columns of a workgroup.  256 columns of outputs and queries leave one wave a SIMD, whose 512 registers hold
-  // them with bf16 caches (750 TFLOP/s); 8-bit ones need more, for what is in flight and converted, and are faster (520
-  // against 380) with two workgroups that have half of the outputs each and both form the scores.
+  // them with bf16 caches but for 35 in scratch (750 TFLOP/s); 8-bit ones need more, for what is in flight and converted,
+  // and are faster (520 against 380) with two workgroups that have half of the outputs each, both form the scores, and
+  // run two waves a SIMD of 256 registers (29 more in scratch).
   static constexpr int DV = D == 256 && Q8 ? 128 : D;
   static constexpr int TK = DV < D ? 32 : 64;  // keys of a tile
   static constexpr int RK = D * 2, RV = DV * 2;  // bytes of a row of keys and of values in LDS
@@ -325,9 +326,12 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
           if constexpr (LSE) le += e;
           // (a hidden key's scale may be anything)
           if constexpr (Q8) e = EDGE && x == -__builtin_inff() ? 0.f : e * vs[r];
-          // Weights enter the product as bf16: each is off by 2^-8 of itself at most, in either direction,
-          // where the output's own rounding is as large.  At the edges, where rows may see a few keys only, what the
-          // rounding leaves follows in a product of its own (2% of a serving step's chunks, nothing of a long prompt).
+          // Weights enter the product as bf16: each is off by 2^-8 of itself at most, in either direction, where the
+          // output's own rounding is as large (8192 tokens after 8192: 0.0023 of the outputs' norm from 64 bits, 0.0017
+          // of it that rounding).  What is left, as a second product for every tile, would take half as many matrix
+          // instructions more: 229 -> 319 us for 4096 tokens after 4096 with 64 columns, 227 -> 274 for 1024 after 8000
+          // with 256, and 128 columns have no registers for it.  At the edges, where rows may see a few keys only, it is
+          // done (2% of a serving step's chunks, nothing of a long prompt).
           bf16 w = (bf16)e;
           // (8-bit values are finite or NaN, and their weights of either sign)
           if constexpr (EDGE && !Q8) w = __builtin_bit_cast(bf16, (unsigned short)(upper_bf16(e) >> 16));

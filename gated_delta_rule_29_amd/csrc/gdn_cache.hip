@@ -8,7 +8,8 @@
 // of pages of 16: 17.5 us, 5.8 TB/s of what it reads and writes, part of it out of the last caches).  Writing 8 bits
 // is bound by its instructions, some 1240 a wave of 16 rows (vector units busy 64%): addresses in 64 bits, the
 // maximum, conversions, and the look through earlier slots (8192 tokens of 8 heads of 128 columns: 21 us, 2.5 TB/s).  16 columns a lane, and
-// neighbouring tokens on one die, were no faster.  Single tokens (64 of them: 4.4 us) are one chain of loads.
+// neighbouring tokens on one die, were no faster.  In the inputs' type they are written in 15.4 us (67 MB, 4.4 TB/s).
+// Single tokens (64 of them: 4.4 us) are one chain of loads.
 #include "../../include/gdn.h"
 #include "gdn_attn.h"
 #include "gdn_layer_device.h"

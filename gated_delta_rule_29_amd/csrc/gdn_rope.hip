@@ -25,7 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxAngles = 4096;  // of a workgroup: cosines and sines in 32 KB of LDS
 
 // Cosine and sine of `turn` * 2^-32 turns.  The remainder's angle is at most pi / 4, where the Taylor
-// polynomials below end at 2e-9 (sine: the term in x^11) and 2e-9 (cosine: x^12), under 2^-24 / 16.
+// polynomials below end at 2e-9 (sine: the term in x^11) and 1e-10 (cosine: x^12), under 2^-24 / 16.
 __device__ __forceinline__ void cos_sin(uint32_t turn, float* c, float* s) {
   const uint32_t q = (turn + (1u << 29)) >> 30;
   const float x = (float)(int32_t)(turn - (q << 30)) * 0x1.921fb6p-30f;  // 2 pi / 2^32

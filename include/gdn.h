@@ -851,7 +851,7 @@ GDN_API int rms_norm_bwd(const void* dy, int64_t dy_pitch, const void* s, int64_
  *   x [T, H, D] dtype;  positions [T] int32 (any value);  y [T, H, D] dtype OUT
  *   table [R / 2] uint64: turns_i in 2^-64 turns a position, so angles are exact to 2^-32 turns at any
  *   position
- * Supported: D <= 1024, even R in 2 .. D.
+ * Supported: D <= 1024, even R in 2 .. D, T * ceil(H * D / 256) < 2^24 (GDN_ERR_INVALID beyond).
  */
 GDN_API int rope_fwd(const void* x, int64_t x_pitch, int64_t x_head_pitch, const int* positions,
                      const uint64_t* table, float magnitude, void* y, int T, int H, int D, int R,
@@ -869,7 +869,7 @@ GDN_API int rope_bwd(const void* dy, int64_t dy_pitch, int64_t dy_head_pitch, co
  *   square of T beyond some ten thousand rows).
  *   e4m3: scale = max(max |x|, 1e-12) / 448 over a token and head's D columns, values e4m3(x / scale) to
  *   nearest even.  A NaN makes its row's scale and values NaN.
- * Supported: D <= 512, H <= 4096.
+ * Supported: D <= 512, H <= 4096, T * H < 2^24 (GDN_ERR_INVALID beyond).
  */
 GDN_API int kv_cache_write(const void* k, int64_t k_pitch, int64_t k_head_pitch, const void* v,
                            int64_t v_pitch, int64_t v_head_pitch, const int* slots, void* k_cache,
@@ -897,7 +897,7 @@ GDN_API int kv_cache_read(const void* k_cache, const void* v_cache, const float*
  *   o [B, T, Hq, D] dtype OUT;  lse [B, T, Hq] fp32 OUT or NULL
  *   workspace  at least paged_attn_workspace_bytes (0 where no keys are cut), 256-byte aligned
  * k_cache, v_cache and o must be 16-byte aligned.  How a call is cut into pieces of keys follows from its
- * sizes and seq_lens; results of another cut differ in fp32 rounding only.
+ * sizes and seq_lens; results of another cut, or with lse, differ in fp32 rounding only.
  * Supported: D 64, 128 or 256; Hq a multiple of Hk; scale > 0.
  */
 GDN_API size_t paged_attn_workspace_bytes(int B, int T, int Hq, int Hk, int D, int P, int max_pages,
