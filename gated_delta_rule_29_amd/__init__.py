@@ -53,11 +53,15 @@ def _cu_pair(cu_seqlens, cu_seqlens_host, dev):
     used as is, so a device cu_seqlens plus its host copy costs no transfer; otherwise the
     missing side is copied (device to host waits for the device)."""
     if cu_seqlens_host is not None:
-        cu_host = torch.as_tensor(cu_seqlens_host, dtype=torch.int32).contiguous()
+        cu_host = torch.as_tensor(cu_seqlens_host)
         if cu_host.device.type != "cpu":
             raise ValueError("cu_seqlens_host must be a host tensor")
     else:
-        cu_host = cu_seqlens.detach().to("cpu", torch.int32).contiguous()
+        cu_host = cu_seqlens.detach().to("cpu")
+    # (the conversion would keep the low bits of larger ones)
+    if cu_host.dtype != torch.int32 and cu_host.numel() and max(int(cu_host.max()), -int(cu_host.min())) > 0x7fffffff:
+        raise ValueError("cu_seqlens holds offsets beyond 32 bits")
+    cu_host = cu_host.to(torch.int32).contiguous()
     if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.device == dev and \
             cu_seqlens.dtype == torch.int32 and cu_seqlens.is_contiguous():
         cu_dev = cu_seqlens

@@ -282,3 +282,22 @@ def test_windows_beyond_32_bits(form, monkeypatch):
     for window in (-1, -2 ** 31 - 1, -2 ** 32, -2 ** 32 + 7, -2 ** 70):
         with pytest.raises(ValueError, match="window"):
             run(window)
+
+
+@pytest.mark.parametrize("bad", [[0, 2 ** 32 + 1, 3], [0, 1, 2 ** 32 + 3], [-2 ** 32, 1, 3], [0, -2 ** 32 + 1, 3]])
+def test_offsets_beyond_32_bits(bad):
+    """Offsets whose low 32 bits would make a good call are refused, as the device's, the host's or both."""
+    import gated_delta_rule_29_amd as g
+
+    cpu = torch.device("cpu")
+    good, wide = torch.tensor([0, 1, 3]), torch.tensor(bad)
+    for args in ((wide, None), (wide, wide), (wide.to(torch.int32), wide), (good, bad)):
+        with pytest.raises(ValueError, match="32 bits"):
+            g._cu_pair(*args, cpu)
+    for args in ((good, None), (good, good), (good.to(torch.int32), [0, 1, 3]), (good, good.numpy())):
+        for t in g._cu_pair(*args, cpu):
+            assert t.dtype == torch.int32 and t.tolist() == [0, 1, 3]
+    c = torch.zeros(5, 2, 16, 64, dtype=torch.bfloat16)
+    t, n = torch.zeros(2, 4, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="32 bits"):
+        g.paged_attn_fwd_varlen(torch.zeros(1, 3, 4, 64, dtype=torch.bfloat16), c, c, t, n, wide)
