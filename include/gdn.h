@@ -891,7 +891,7 @@ GDN_API int kv_cache_read(const void* k_cache, const void* v_cache, const float*
  * included.
  *   q [B, T, Hq, D] dtype (tokens evenly spaced);  query heads h * Hq / Hk .. share key head h
  *   block_table [B, max_pages] int32 (rows table_pitch apart): page of a sequence's places 0 .. P - 1,
- *   P .. 2 P - 1, ..; entries behind its length are not read.  A page outside [0, pages) reads as keys and
+ *   P .. 2 P - 1, ..; entries behind its length do not matter.  A page outside [0, pages) reads as keys and
  *   values of 0.
  *   seq_lens [B] int32 (device): keys of each sequence; taken as the nearest number in [0, max_pages * P]
  *   o [B, T, Hq, D] dtype OUT;  lse [B, T, Hq] fp32 OUT or NULL
