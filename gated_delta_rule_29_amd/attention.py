@@ -303,7 +303,8 @@ def paged_attn_fwd_varlen(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens
     n = _lib.load().paged_attn_varlen_workspace_bytes(host.data_ptr(), N, *ws_sizes)
     ws = _workspace(n, dev)
     _call("paged_attn_fwd_varlen", dev, *args, cu.data_ptr(), host.data_ptr(), N, scale, 1 if causal else 0,
-          _window(window), o.data_ptr(), lse.data_ptr() if want_lse else None, T, *sizes, ws.data_ptr() if n else None, n)
+          _window(window), o.data_ptr(), lse.data_ptr() if want_lse else None, T, *sizes, ws.data_ptr() if n else None,
+          n)
     return {"o": o, "lse": lse} if want_lse else {"o": o}
 
 
@@ -320,5 +321,6 @@ def paged_attn_step(q, k_cache, v_cache, block_table, seq_lens, k_scale=None, v_
     o = _like(q)
     n = _lib.load().paged_attn_workspace_bytes(B, 1, *ws_sizes)
     ws = _workspace(n, dev)
-    _call("paged_attn_step", dev, *args, scale, _window(window), o.data_ptr(), B, *sizes, ws.data_ptr() if n else None, n)
+    _call("paged_attn_step", dev, *args, scale, _window(window), o.data_ptr(), B, *sizes, ws.data_ptr() if n else None,
+          n)
     return o

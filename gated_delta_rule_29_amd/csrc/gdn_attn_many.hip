@@ -11,10 +11,10 @@
 //
 // 8192 tokens after 8192, 32 query and 8 key heads of 128 columns, bf16: 1370 to 1450 us by the card's clock,
 // 1.14 to 1.2 PFLOP/s of the keys that are seen, where a large library product reaches 1.21.  Bound by instruction
-// issue: a tile of 64 keys is 32 products of 32 cycles and some 140 other vector instructions a wave, and a product keeps
-// the other wave's from issuing for about half of its time; matrix units are busy 59 to 61% of the time.
-// Of 4096 tokens after 4096 (TFLOP/s): 128 columns over 8 bits 735 (two multiplications more for each score, 5 registers in
-// scratch, and one tile a stage); 64 columns 850, over 8 bits 690; 256 columns 700 to 750, over 8 bits 510.  Tiles of 128 rows of four waves, two groups of waves that take turns at products and
+// issue: a tile of 64 keys is 32 products of 32 cycles and some 140 other vector instructions a wave, and a product
+// keeps the other wave's from issuing for about half of its time; matrix units are busy 59 to 61% of the time.
+// Of 4096 tokens after 4096 (TFLOP/s): 128 columns over 8 bits 735 (two multiplications more for each score, 5
+// registers in scratch, and one tile a stage); 64 columns 850, over 8 bits 690; 256 columns 700 to 750, over 8 bits 510.  Tiles of 128 rows of four waves, two groups of waves that take turns at products and
 // exponentials (1552 us), and both interleaved by hand in a wave (1621) were no faster.
 #include "../../include/gdn.h"
 #include "gdn_attn_device.h"
@@ -343,12 +343,14 @@ __global__ __launch_bounds__(64 * NW) void attn_many_kernel(AttnParams p) {
         }
       }
     if constexpr (!EDGE && AS_THEY_ENTER) {
+      // (two weights and the sum are rounded once, to nearest)
       typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
       const bf16x2 one = {(bf16)1.f, (bf16)1.f};
 #pragma unroll
       for (int s = 0; s < PS; ++s)
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pf[s][j], pf[s][j + 1]}, one, l, false);
+        for (int j = 0; j < 8; j += 2)
+          l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{pf[s][j], pf[s][j + 1]}, one, l, false);
     }
     auto values = [&](int s, int b) {
       const int x = VP == 1 ? 64 * b : 0, off = sub * M::VT + 16 * s * RV;
